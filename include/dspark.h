@@ -71,12 +71,14 @@ typedef enum {
   DSPARK_ERR_DEVICE_TIMEOUT = 11, /* device: a bounded wait inside a kernel gave up      */
   DSPARK_ERR_CUDA = 12,           /* a CUDA runtime call failed (launch, query, copy)    */
   DSPARK_ERR_UNSUPPORTED = 13,    /* the current device is not sm_103 / shape unsupported */
-  DSPARK_ERR_BOUNDS = 14          /* device, bounds-checked build only: an index the kernels
+  DSPARK_ERR_BOUNDS = 14,         /* device, bounds-checked build only: an index the kernels
                                      computed fell outside its buffer (the access was sent to
                                      element 0 instead); never returned by the normal build */
+  DSPARK_ERR_PAGES = 15           /* device: a page id outside [0, pages)                */
 } dspark_status;
 
-typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
+/* DSPARK_F16: the operators on heads only (norm_rope, append, attention) */
+typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2 } dspark_dtype;
 
 /* dims.flags bits */
 #define DSPARK_FLAG_FORCE_SIMT 1u /* draft: use the CUDA-core bias path even when the tensor-core path applies */
@@ -435,6 +437,116 @@ dspark_status dspark_verify_markov(const void *U, const void *E, const void *W, 
                                    const int32_t *draft_tok, const float *temperature, uint64_t seed,
                                    dspark_dims dims, int32_t *n_acc, int32_t *out_tok, void *workspace,
                                    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The operators around a ragged verification step.  A target model that verifies
+ * drafted tokens runs its layers over the same ragged rows as dspark_verify_ragged:
+ * request r owns rows row_off[r] .. row_off[r+1]-1 (the scheduler's tgt_off), which
+ * are the last n_r of its kv_len[r] tokens.  Per layer: norm and rotate the heads,
+ * append keys and values to the cache, attend; after the head, penalise the logits
+ * and verify.  Rows at and past row_off[B] are left alone, so that the buffers (and a
+ * captured graph) can be sized for the largest step.
+ * ------------------------------------------------------------------------ */
+
+/* Heads: element (row, head, dim) at row * row_stride + head * head_stride + dim, e.g. the
+ * parts of a fused projection's output.  data 16-byte aligned, strides multiples of 16 bytes. */
+typedef struct {
+  const void *data;
+  int64_t row_stride, head_stride;   /* in elements */
+} dspark_heads;
+
+/* Rotation of the first rotary_dim dimensions of a head (a multiple of 16).  Pair i is
+ * dimensions (i, i + rotary_dim/2), or (2i, 2i + 1) when interleaved; it turns by
+ * position * inv_freq_i and is scaled by gain.  turns[i] = round(inv_freq_i / (2 pi) * 2^64)
+ * modulo 2^64: the turn per position in fixed point, so that the angle is exact to
+ * 2^-32 turns at any position.  Scalings for long contexts are the caller's choice of turns and gain. */
+typedef struct {
+  const uint64_t *turns;             /* device [rotary_dim / 2] */
+  int32_t rotary_dim, interleaved;
+  float gain;
+} dspark_rope;
+
+/* A paged key/value cache in 4 bits: [pages][kv_heads][page_size / 16][18 head_dim] bytes.
+ * A tile of 16 tokens of one head (D = head_dim, w = D/16) holds
+ *   [0, 8D)    keys: token t at t D/2, two e2m1 codes a byte, the even dimension low;
+ *   [8D, 16D)  values: chunk c (dimensions 2wc .. 2wc+2w-1) of token t at w (64 (t/8) + 8c + t%8);
+ *   [16D, 17D) key scales, e4m3, one for 16 dimensions: token t, group c at t w + c;
+ *   [17D, 18D) value scales: token t, group c at (t/8) D/2 + 8c + t%8.
+ * An element's value is e2m1 * e4m3 * k_scale (or v_scale).  head_dim 64 or 128; page_size a
+ * multiple of 16 to 4096; k_scale and v_scale powers of two; data 16-byte aligned. */
+typedef struct {
+  void *data;
+  int64_t pages;
+  int32_t kv_heads, head_dim, page_size;
+  float k_scale, v_scale;
+} dspark_cache;
+
+/* Ragged rows over the cache.  row_off [B+1] int32; kv_len [B] int32, a request's tokens in the
+ * cache with this step's rows among them; page_table [B, max_pages] int32 page ids, entries past a
+ * request's last page are not read; rows: the rows of the call's tensors, >= row_off[B].
+ * Row j of request r is token kv_len[r] - n_r + j, n_r = row_off[r+1] - row_off[r]. */
+typedef struct {
+  const int32_t *row_off, *kv_len, *page_table;
+  int64_t B, rows, max_pages;
+} dspark_ragged;
+
+/* y = x rsqrt(mean(x^2) + eps) weight per head (where a weight [head_dim] of the call's dtype is
+ * given), then the rotation (rope NULL: none), in fp32, rounded once.  q_out [rows, q_heads, D] and
+ * k_out [rows, kv_heads, D] are contiguous and may be the inputs themselves when those are; k and k_out may be NULL.
+ * positions [rows] int32.  head_dim: a multiple of 16 to 256.  F32, BF16, F16. */
+dspark_status dspark_attn_norm_rope(const dspark_heads *q, const dspark_heads *k, int64_t rows, int32_t q_heads,
+                                    int32_t kv_heads, int32_t head_dim, int32_t dtype, const int32_t *positions,
+                                    const dspark_rope *rope, const void *q_weight, const void *k_weight, float eps,
+                                    void *q_out, void *k_out, int32_t *dev_status, void *stream);
+
+/* Append k and v [rows, kv_heads, D] to the cache: keys normed and rotated as above, then both
+ * quantised: scale = e4m3(max |y| / 6) over 16 dimensions of y / k_scale (or v_scale), element =
+ * e2m1(y / scale), both to nearest, ties to even, saturating; a group with a NaN gets the scale NaN.
+ * With q [rows, q_heads, D] the queries are normed and rotated in the same pass into q_out.
+ * positions NULL: a row's rotary position is its place in the cache.  F32, BF16, F16.
+ * Device errors: OFFSETS (row_off), LENGTHS (a row before token 0 or past the page table), PAGES. */
+dspark_status dspark_attn_append(const dspark_heads *k, const dspark_heads *v, const dspark_heads *q, int32_t q_heads,
+                                 int32_t dtype, const dspark_cache *cache, const dspark_ragged *where,
+                                 const int32_t *positions, const dspark_rope *rope, const void *q_weight,
+                                 const void *k_weight, float eps, void *q_out, int32_t *dev_status, void *stream);
+
+/* What the cache holds of the rows' tokens: elements [rows, kv_heads, D] and scales
+ * [rows, kv_heads, D/16] of keys and values, as e4m3 bytes (exact). */
+dspark_status dspark_attn_cache_read(const dspark_cache *cache, const dspark_ragged *where, void *k, void *k_scale,
+                                     void *v, void *v_scale, int32_t *dev_status, void *stream);
+
+/* out [rows, q_heads, D] = softmax(scale q.k) v over the tokens that a row sees, query head i with
+ * key/value head i / (q_heads / kv_heads).  Row j of request r sees tokens t < hi, hi = kv_len[r]
+ * (causal: kv_len[r] - n_r + j + 1), and with window > 0 only t >= hi - window.  A row that sees
+ * nothing gets 0 and lse -inf.  lse [rows, q_heads] float, optional: log sum exp(scale q.k).
+ * max_rows: no request has more rows (sizes the launch; a larger one is DSPARK_ERR_LENGTHS).
+ * BF16, F16.  No workspace. */
+dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t dtype, const dspark_cache *cache,
+                                const dspark_ragged *where, int64_t max_rows, float scale, int32_t causal,
+                                int64_t window, void *out, float *lse, int32_t *dev_status, void *stream);
+
+/* Penalties, biases and masks of the logits' rows. */
+typedef struct {
+  const int32_t *hist;               /* [B, hist_cap] token ids: the prompt, then the output so far       */
+  const int32_t *hist_len;           /* [B] tokens in hist                                              */
+  const int32_t *prompt_len;         /* [B] how many of them are the prompt's                            */
+  const int32_t *draft_tok;          /* [B, draft_cap] or NULL: row j counts draft tokens 0 .. j-1 as output */
+  const float *repetition, *presence, *frequency;   /* [B]                                              */
+  const int32_t *bias_tok;           /* [B, bias_cap], -1 pads; a token listed twice gets the sum         */
+  const float *bias_val;             /* [B, bias_cap]                                                   */
+  const void *mask;                  /* [rows, (V+31)/32] 32-bit words or NULL: bit v%32 of word v/32 allows v */
+  int64_t hist_cap, draft_cap, bias_cap;
+} dspark_penalties;
+
+/* out[i, v] for row i = row_off[r] + j, with n the count of v in the request's output and draft
+ * tokens, s whether v is in its prompt:
+ *   z = logits[i, v];  n > 0 or s: z = z > 0 ? z / repetition : z * repetition;
+ *   z -= presence [n > 0] + frequency n;  z += bias of v;  -inf where the mask forbids v
+ * in fp32, rounded once.  out may be logits.  F32, BF16; [rows, V] contiguous.  A mask that allows
+ * nothing leaves a row of -inf. */
+dspark_status dspark_logits_penalize(const void *logits, int32_t dtype, int64_t rows, int64_t V, int64_t B,
+                                     const int32_t *row_off, const dspark_penalties *p, void *out,
+                                     int32_t *dev_status, void *stream);
 
 /* ------------------------------------------------------------------------
  * Status helpers.

@@ -24,14 +24,15 @@ __all__ = [
     "verify_ragged", "check", "status_string", "draft_workspace_bytes", "schedule_workspace_bytes",
     "verify_workspace_bytes", "F32", "BF16", "FLAG_FORCE_SIMT", "FLAG_W_PACKED", "FLAG_SPARE_SM", "STATUS_NAMES", "Dims",
     "PackedProjection", "pack_projection", "packed_projection_bytes", "verify_markov",
-    "verify_markov_workspace_bytes",
+    "verify_markov_workspace_bytes", "Rope", "PagedCache", "norm_rope", "cache_append", "cache_read", "attend_paged",
+    "penalize_logits", "F16",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # DSPARK_LIBRARY selects another build of the same library (the bounds-checked one in tests)
 _LIB_PATH = os.environ.get("DSPARK_LIBRARY") or os.path.join(_HERE, "libdspark.so")
 
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
 FLAG_FORCE_SIMT = 1
 FLAG_W_PACKED = 2
 FLAG_SPARE_SM = 4
@@ -42,7 +43,7 @@ STATUS_NAMES = {
     4: "DSPARK_ERR_TEMPERATURE", 5: "DSPARK_ERR_SPS_TOO_SHORT", 6: "DSPARK_ERR_OFFSETS",
     7: "DSPARK_ERR_TOKEN_RANGE", 8: "DSPARK_ERR_LENGTHS", 9: "DSPARK_ERR_CONFIDENCE",
     10: "DSPARK_ERR_WORKSPACE", 11: "DSPARK_ERR_DEVICE_TIMEOUT", 12: "DSPARK_ERR_CUDA",
-    13: "DSPARK_ERR_UNSUPPORTED", 14: "DSPARK_ERR_BOUNDS",
+    13: "DSPARK_ERR_UNSUPPORTED", 14: "DSPARK_ERR_BOUNDS", 15: "DSPARK_ERR_PAGES",
 }
 
 EXPORTED_SYMBOLS = [
@@ -52,7 +53,8 @@ EXPORTED_SYMBOLS = [
     "dspark_schedule_survival", "dspark_schedule_survival_noalloc", "dspark_schedule_capacity",
     "dspark_schedule_topk", "dspark_schedule_threshold", "dspark_verify_workspace_bytes",
     "dspark_verify_ragged", "dspark_verify_markov_workspace_bytes", "dspark_verify_markov",
-    "dspark_status_string", "dspark_check", "dspark_version",
+    "dspark_attn_norm_rope", "dspark_attn_append", "dspark_attn_cache_read", "dspark_attn_paged",
+    "dspark_logits_penalize", "dspark_status_string", "dspark_check", "dspark_version",
 ]
 
 
@@ -130,6 +132,7 @@ def lib() -> ctypes.CDLL:
     L.dspark_check.restype = st
     L.dspark_version.argtypes = []
     L.dspark_version.restype = ctypes.c_int
+    serving.declare(L)
     _lib = L
     return L
 
@@ -546,3 +549,7 @@ def verify_markov(U, E, W, anchor, draft_lse, draft_tok_logit, tgt_logits, tgt_o
                                       ctypes.c_size_t(ws.numel()), _ptr(status), _stream(stream))
     _raise(code, "dspark_verify_markov")
     return dict(n_acc=n_acc, out_tok=out_tok, status=status, workspace=ws)
+
+
+from . import serving  # noqa: E402
+from .serving import PagedCache, Rope, attend_paged, cache_append, cache_read, norm_rope, penalize_logits  # noqa: E402

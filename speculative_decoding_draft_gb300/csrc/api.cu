@@ -6,6 +6,9 @@
 #include <map>
 #include <utility>
 
+#include <cmath>
+
+#include "attn.cuh"
 #include "schedule.cuh"
 
 using namespace dspark;
@@ -98,6 +101,7 @@ const char *dspark_status_string(dspark_status s) {
     case DSPARK_ERR_CUDA: return "DSPARK_ERR_CUDA";
     case DSPARK_ERR_UNSUPPORTED: return "DSPARK_ERR_UNSUPPORTED";
     case DSPARK_ERR_BOUNDS: return "DSPARK_ERR_BOUNDS";
+    case DSPARK_ERR_PAGES: return "DSPARK_ERR_PAGES";
   }
   return "DSPARK_ERR_UNKNOWN";
 }
@@ -556,6 +560,202 @@ dspark_status dspark_verify_markov(const void *U, const void *E, const void *W, 
   if (!(dims.flags & DSPARK_FLAG_W_PACKED) && launch_pack_projection(W, dims.rank, dims.V, (void *)r.Wp, s) != cudaSuccess)
     return DSPARK_ERR_CUDA;
   return launch_verify(a, s, dev.sms, &r) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// heads, paged cache, attention, penalties
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxRows = 0x7fffffff;
+constexpr int64_t kMaxHeads = 1024;
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+bool power_of_two(float x) {
+  int e;
+  return std::isfinite(x) && x > 0.0f && std::frexp(x, &e) == 0.5f && e > -60 && e < 60;
+}
+
+size_t dtype_bytes(int dtype) { return dtype == DSPARK_F32 ? 4 : 2; }
+
+// A tensor of heads: rows 16-byte aligned whatever the row and head.
+dspark_status check_heads(const dspark_heads &t, int dtype) {
+  if (!t.data) return DSPARK_ERR_NULL;
+  const int64_t unit = 16 / (int64_t)dtype_bytes(dtype);
+  if (t.row_stride < 0 || t.head_stride < 0) return DSPARK_ERR_DIMS;
+  if (!aligned16(t.data) || t.row_stride % unit || t.head_stride % unit) return DSPARK_ERR_UNSUPPORTED;
+  return DSPARK_OK;
+}
+
+dspark_status check_rope(const dspark_rope *rope, int head_dim) {
+  if (!rope) return DSPARK_OK;
+  if (!rope->turns) return DSPARK_ERR_NULL;
+  if (rope->rotary_dim < 16 || rope->rotary_dim % 16 || rope->rotary_dim > head_dim) return DSPARK_ERR_DIMS;
+  if (!std::isfinite(rope->gain)) return DSPARK_ERR_DIMS;
+  return DSPARK_OK;
+}
+
+dspark_status check_cache(const dspark_cache *c) {
+  if (!c || !c->data) return DSPARK_ERR_NULL;
+  if (c->pages < 1 || c->pages > ((int64_t)1 << 40) || c->kv_heads < 1 || c->kv_heads > kMaxHeads) return DSPARK_ERR_DIMS;
+  if (c->page_size < 16 || c->page_size % 16 || c->page_size > 4096) return DSPARK_ERR_DIMS;
+  if (c->head_dim != 64 && c->head_dim != 128) return DSPARK_ERR_UNSUPPORTED;
+  if (!power_of_two(c->k_scale) || !power_of_two(c->v_scale)) return DSPARK_ERR_DIMS;
+  return aligned16(c->data) ? DSPARK_OK : DSPARK_ERR_UNSUPPORTED;
+}
+
+dspark_status check_ragged(const dspark_ragged *t) {
+  if (!t || !t->row_off || !t->kv_len || !t->page_table) return DSPARK_ERR_NULL;
+  if (t->B < 1 || t->B > kMaxB || t->rows < 1 || t->rows > kMaxRows || t->max_pages < 1 || t->max_pages > kMaxRows)
+    return DSPARK_ERR_DIMS;
+  return DSPARK_OK;
+}
+
+bool right_device() {
+  DeviceInfo d;
+  return device_info(&d) && d.major == 10 && d.minor == 3;
+}
+
+}  // namespace
+
+dspark_status dspark_attn_norm_rope(const dspark_heads *q, const dspark_heads *k, int64_t rows, int32_t q_heads,
+                                    int32_t kv_heads, int32_t head_dim, int32_t dtype, const int32_t *positions,
+                                    const dspark_rope *rope, const void *q_weight, const void *k_weight, float eps,
+                                    void *q_out, void *k_out, int32_t *dev_status, void *stream) {
+  if (!q || !q_out || !dev_status || (rope && !positions)) return DSPARK_ERR_NULL;
+  if ((k != nullptr) != (k_out != nullptr)) return DSPARK_ERR_NULL;
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_DTYPE;
+  if (rows < 1 || rows > kMaxRows || q_heads < 1 || q_heads > kMaxHeads || head_dim < 16 || head_dim > 256 ||
+      head_dim % 16 || (k && (kv_heads < 1 || kv_heads > kMaxHeads)) || !(eps >= 0.0f))
+    return DSPARK_ERR_DIMS;
+  dspark_status st = check_heads(*q, dtype);
+  if (st == DSPARK_OK && k) st = check_heads(*k, dtype);
+  if (st == DSPARK_OK) st = check_rope(rope, head_dim);
+  if (st != DSPARK_OK) return st;
+  if (!aligned16(q_out) || !aligned16(k_out)) return DSPARK_ERR_UNSUPPORTED;
+  if (!right_device()) return DSPARK_ERR_UNSUPPORTED;
+  HeadsArgs a = {};
+  a.q = q->data, a.q_row = q->row_stride, a.q_head = q->head_stride;
+  if (k) a.k = k->data, a.k_row = k->row_stride, a.k_head = k->head_stride;
+  a.q_out = q_out, a.k_out = k_out;
+  a.q_weight = q_weight, a.k_weight = k_weight;
+  a.positions = positions;
+  if (rope) {
+    a.turns = (const unsigned long long *)rope->turns;
+    a.rot = rope->rotary_dim, a.interleaved = rope->interleaved != 0, a.gain = rope->gain;
+  }
+  a.rows = rows, a.Hq = q_heads, a.Hkv = k ? kv_heads : 0, a.D = head_dim, a.dtype = dtype, a.eps = eps;
+  a.dev_status = dev_status;
+  return launch_norm_rope(a, (cudaStream_t)stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+dspark_status dspark_attn_append(const dspark_heads *k, const dspark_heads *v, const dspark_heads *q, int32_t q_heads,
+                                 int32_t dtype, const dspark_cache *cache, const dspark_ragged *where,
+                                 const int32_t *positions, const dspark_rope *rope, const void *q_weight,
+                                 const void *k_weight, float eps, void *q_out, int32_t *dev_status, void *stream) {
+  if (!k || !v || !dev_status || (q != nullptr) != (q_out != nullptr)) return DSPARK_ERR_NULL;
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_DTYPE;
+  dspark_status st = check_cache(cache);
+  if (st == DSPARK_OK) st = check_ragged(where);
+  if (st == DSPARK_OK) st = check_heads(*k, dtype);
+  if (st == DSPARK_OK) st = check_heads(*v, dtype);
+  if (st == DSPARK_OK && q) st = check_heads(*q, dtype);
+  if (st == DSPARK_OK) st = check_rope(rope, cache->head_dim);
+  if (st != DSPARK_OK) return st;
+  if ((q && (q_heads < 1 || q_heads > kMaxHeads)) || !(eps >= 0.0f)) return DSPARK_ERR_DIMS;
+  if (!aligned16(q_out)) return DSPARK_ERR_UNSUPPORTED;
+  if (!right_device()) return DSPARK_ERR_UNSUPPORTED;
+  HeadsArgs a = {};
+  if (q) a.q = q->data, a.q_row = q->row_stride, a.q_head = q->head_stride;
+  a.k = k->data, a.k_row = k->row_stride, a.k_head = k->head_stride;
+  a.v = v->data, a.v_row = v->row_stride, a.v_head = v->head_stride;
+  a.q_out = q_out;
+  a.q_weight = q ? q_weight : nullptr, a.k_weight = k_weight;
+  a.positions = positions;
+  if (rope) {
+    a.turns = (const unsigned long long *)rope->turns;
+    a.rot = rope->rotary_dim, a.interleaved = rope->interleaved != 0, a.gain = rope->gain;
+  }
+  a.rows = where->rows, a.Hq = q ? q_heads : 0, a.Hkv = cache->kv_heads, a.D = cache->head_dim, a.dtype = dtype;
+  a.eps = eps;
+  a.cache = (uint8_t *)cache->data, a.pages = cache->pages, a.page_size = cache->page_size;
+  a.k_inv = 1.0f / cache->k_scale, a.v_inv = 1.0f / cache->v_scale;
+  a.B = where->B, a.max_pages = where->max_pages;
+  a.row_off = where->row_off, a.kv_len = where->kv_len, a.table = where->page_table;
+  a.dev_status = dev_status;
+  return launch_cache_append(a, (cudaStream_t)stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+dspark_status dspark_attn_cache_read(const dspark_cache *cache, const dspark_ragged *where, void *k, void *k_scale,
+                                     void *v, void *v_scale, int32_t *dev_status, void *stream) {
+  if (!k || !k_scale || !v || !v_scale || !dev_status) return DSPARK_ERR_NULL;
+  dspark_status st = check_cache(cache);
+  if (st == DSPARK_OK) st = check_ragged(where);
+  if (st != DSPARK_OK) return st;
+  if (!aligned16(k) || !aligned16(v)) return DSPARK_ERR_UNSUPPORTED;
+  if (!right_device()) return DSPARK_ERR_UNSUPPORTED;
+  CacheReadArgs a = {};
+  a.cache = (const uint8_t *)cache->data, a.pages = cache->pages, a.page_size = cache->page_size;
+  a.Hkv = cache->kv_heads, a.D = cache->head_dim;
+  a.B = where->B, a.rows = where->rows, a.max_pages = where->max_pages;
+  a.row_off = where->row_off, a.kv_len = where->kv_len, a.table = where->page_table;
+  a.k = (uint8_t *)k, a.ks = (uint8_t *)k_scale, a.v = (uint8_t *)v, a.vs = (uint8_t *)v_scale;
+  a.dev_status = dev_status;
+  return launch_cache_read(a, (cudaStream_t)stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t dtype, const dspark_cache *cache,
+                                const dspark_ragged *where, int64_t max_rows, float scale, int32_t causal,
+                                int64_t window, void *out, float *lse, int32_t *dev_status, void *stream) {
+  if (!q || !out || !dev_status) return DSPARK_ERR_NULL;
+  if (dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_DTYPE;
+  dspark_status st = check_cache(cache);
+  if (st == DSPARK_OK) st = check_ragged(where);
+  if (st == DSPARK_OK) st = check_heads(*q, dtype);
+  if (st != DSPARK_OK) return st;
+  // token positions are 32-bit inside the kernel
+  if (q_heads < 1 || q_heads > kMaxHeads || q_heads % cache->kv_heads || max_rows < 1 || max_rows > (1 << 20) ||
+      !std::isfinite(scale) || window < 0 || window > kMaxRows || where->max_pages * cache->page_size > kMaxRows)
+    return DSPARK_ERR_DIMS;
+  if (!aligned16(out)) return DSPARK_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return DSPARK_ERR_CUDA;
+  if (dev.major != 10 || dev.minor != 3) return DSPARK_ERR_UNSUPPORTED;
+  AttendArgs a = {};
+  a.q = q->data, a.q_row = q->row_stride, a.q_head = q->head_stride;
+  a.out = out, a.lse = lse;
+  a.cache = (const uint8_t *)cache->data, a.pages = cache->pages, a.page_size = cache->page_size;
+  a.Hq = q_heads, a.Hkv = cache->kv_heads, a.D = cache->head_dim, a.group = q_heads / cache->kv_heads;
+  a.B = where->B, a.rows = where->rows, a.max_pages = where->max_pages;
+  a.row_off = where->row_off, a.kv_len = where->kv_len, a.table = where->page_table;
+  a.causal = causal != 0, a.window = (int)window, a.max_rows = (int)(max_rows < where->rows ? max_rows : where->rows);
+  a.dtype = dtype;
+  a.scale_log2 = scale * cache->k_scale * kLog2e;
+  a.out_scale = cache->v_scale;
+  a.dev_status = dev_status;
+  return launch_attend(a, (cudaStream_t)stream, dev.sms) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+dspark_status dspark_logits_penalize(const void *logits, int32_t dtype, int64_t rows, int64_t V, int64_t B,
+                                     const int32_t *row_off, const dspark_penalties *p, void *out,
+                                     int32_t *dev_status, void *stream) {
+  if (!logits || !row_off || !p || !out || !dev_status || !p->hist || !p->hist_len || !p->prompt_len ||
+      !p->repetition || !p->presence || !p->frequency || (p->bias_cap > 0 && (!p->bias_tok || !p->bias_val)))
+    return DSPARK_ERR_NULL;
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return DSPARK_ERR_DTYPE;
+  if (rows < 1 || rows > kMaxRows || V < 2 || V > kMaxV || B < 1 || B > kMaxB || p->hist_cap < 1 ||
+      (V + 4095) / 4096 * B > kMaxRows || p->hist_cap > kMaxRows || p->bias_cap < 0 || p->bias_cap > 4096 || (p->draft_tok && p->draft_cap < 1))
+    return DSPARK_ERR_DIMS;
+  if (!right_device()) return DSPARK_ERR_UNSUPPORTED;
+  PenalizeArgs a = {};
+  a.logits = logits, a.out = out, a.dtype = dtype, a.rows = rows, a.B = B, a.V = V;
+  a.row_off = row_off, a.hist = p->hist, a.hist_len = p->hist_len, a.prompt_len = p->prompt_len;
+  a.hist_cap = p->hist_cap, a.draft_tok = p->draft_tok, a.draft_cap = p->draft_cap;
+  a.bias_tok = p->bias_tok, a.bias_val = p->bias_val, a.bias_cap = p->bias_cap;
+  a.mask = (const uint32_t *)p->mask, a.mask_words = (V + 31) / 32;
+  a.repetition = p->repetition, a.presence = p->presence, a.frequency = p->frequency;
+  a.dev_status = dev_status;
+  return launch_penalize(a, (cudaStream_t)stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // extern "C"

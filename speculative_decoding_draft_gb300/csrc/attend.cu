@@ -1,0 +1,594 @@
+// Attention of ragged rows over a paged cache held in 4 bits.
+//
+//   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q.k_t - m),  lse = m + log sum_t p_t
+// over the tokens t that a row sees: t < hi, hi = kv_len (causal: kv_len - n + j + 1 for row j of n),
+// and t >= hi - window with a window.  A row that sees nothing gets 0 and lse = -inf.
+//
+// One pass over the cache.  A warp takes 32 tokens (two tiles) at a time, brought by bulk copies into
+// a ring of its own, and works transposed: S^T = K Q^T and O^T = V^T P^T with m16n8k16 products, so
+// the tokens (then the dimensions) fill the 16-wide side and the 8-wide side holds the rows: the
+// query heads of one key/value head times the request's rows, 8 for plain decoding with up to 8
+// heads a group, with nothing padded to 16, 64 or 128.  The 4-bit operands go straight from shared
+// memory into the registers of the product: the layout of a tile gives each thread its own bytes, a
+// hardware conversion makes two fp16 of a byte and one multiplication by the scale makes the exact
+// element.  Both inner orders are free (the dimensions of q.k, the dimensions of the output), which
+// is what lets a thread take neighbouring bytes.  P^T is turned into the second product's operand
+// with one matrix transposition in registers per 8x8.
+//
+// Rounding: queries are scaled by a power of two to below 2^9 and rounded to fp16 (exact for bf16 and
+// fp16 queries down to 2^-33 of the row's largest), keys and values are exact, probabilities are
+// rounded to fp16 (2^-12), everything else and all sums are fp32.
+//
+// The running maximum moves only when a score passes it by 2^8: probabilities then lie below 2^14
+// (they are kept 2^6 up so that small ones stay normal fp16 numbers), the result is the same, and the
+// reductions over lanes and the rescaling of the output leave the common path.
+//
+// The tokens of one (request, key/value head, row tile) are dealt to the warps of a cluster of CTAs;
+// partial results meet in shared memory, first of the CTA, then across the cluster.
+#include <cooperative_groups.h>
+
+#include "attn.cuh"
+
+namespace dspark {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kWarps = 8;
+constexpr int kChunk = 32;            // tokens of a warp's step: two tiles
+constexpr float kLazy = 8.0f;         // how far (log2) a score may pass the running maximum
+constexpr float kLift = 6.0f;         // probabilities are kept 2^kLift up
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// The four bytes of a word, each two e2m1 codes, as four pairs of fp16.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 x, y, z, t;\n\t"
+      "mov.b32 {x, y, z, t}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, x;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, y;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, z;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, t;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(h) : "r"(two));
+  return h;
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("mul.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t c;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(c) : "f"(hi), "f"(lo));
+  return c;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[BYTES / 4]) {
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr));
+  else
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+template <int D, int NT, int STAGES>
+struct Shape {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStage = 2 * tile_bytes(D);
+  static constexpr int kRing = STAGES * kStage;                    // per warp
+  static constexpr int kOutRow = D + 4;                            // floats; padded against bank conflicts
+  static constexpr int kOut = kRows * kOutRow * 4;                 // one warp's partial output
+  static constexpr int kWarpBytes = (kRing > kOut ? kRing : kOut); // the ring is reused for it
+  static constexpr bool kQShared = NT > 1;                         // query fragments in shared memory
+  static constexpr int kQ = kQShared ? NT * (D / 16) * 32 * 8 : 0;
+  static constexpr int kBars = kWarps * STAGES * 8;
+  static constexpr int kMl = kWarps * kRows * 8 + kRows * 8;       // maxima and sums of the warps, of the CTA
+  static constexpr int kSmem = kWarps * kWarpBytes + kQ + kBars + kMl + 16;
+};
+
+template <int DT, int D, int NT, int STAGES, int MINB>
+__global__ void __launch_bounds__(kWarps * 32, MINB) attend_kernel(const __grid_constant__ AttendArgs a, int row_tiles) {
+  using T = typename Elem<DT>::T;
+  using Sh = Shape<D, NT, STAGES>;
+  constexpr int KS = D / 16;                 // k-steps of q.k, and m-tiles of the output
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t *q_smem = smem + kWarps * Sh::kWarpBytes;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(q_smem + Sh::kQ);
+  float *warp_m = reinterpret_cast<float *>(bars + kWarps * STAGES);
+  float *warp_l = warp_m + kWarps * Sh::kRows;
+  float *cta_m = warp_l + kWarps * Sh::kRows, *cta_l = cta_m + Sh::kRows;
+  volatile int *abort = reinterpret_cast<volatile int *>(cta_l + Sh::kRows);
+
+  cg::cluster_group cluster = cg::this_cluster();
+  const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
+  int64_t unit = blockIdx.x / cs;
+  const int rt = (int)(unit % row_tiles);
+  unit /= row_tiles;
+  const int h = (int)(unit % a.Hkv);
+  const int64_t r = unit / a.Hkv;
+  const int64_t row0 = a.row_off[r], row1 = a.row_off[r + 1], kv = a.kv_len[r];
+  const int64_t n = row1 - row0;
+  // every CTA of a cluster takes the same way out here
+  if (row0 < 0 || n < 0 || row1 > a.rows) {
+    if (tid == 0) set_status(a.dev_status, DSPARK_ERR_OFFSETS);
+    return;
+  }
+  if (kv < 0 || kv > a.max_pages * a.page_size || n > a.max_rows) {
+    if (tid == 0) set_status(a.dev_status, DSPARK_ERR_LENGTHS);
+    return;
+  }
+  const int first = rt * Sh::kRows, total = (int)n * a.group;
+  if (first >= total) return;
+  const int last = (first + Sh::kRows < total ? first + Sh::kRows : total) - 1;
+  // a step that failed does no work, but its CTAs still meet their cluster below
+  const bool skip = read_status(a.dev_status) != 0;
+
+  // what the tile's rows see: from [lo_min, lo_max] up to [hi_min, hi_max]
+  const int ctx = (int)(kv - n);
+  const int hi_min = a.causal ? ctx + first / a.group + 1 : (int)kv;
+  const int hi_max = a.causal ? ctx + last / a.group + 1 : (int)kv;
+  const int lo_min = a.window ? max(0, hi_min - a.window) : 0, lo_max = a.window ? max(0, hi_max - a.window) : 0;
+  const int c0 = lo_min / kChunk;
+  const int chunks = skip || hi_max <= 0 ? 0 : (hi_max + kChunk - 1) / kChunk - c0;
+
+  const uint32_t ring = smem_u32(smem) + warp * Sh::kWarpBytes;
+  const uint32_t bar = smem_u32(bars + warp * STAGES);
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(bar + 8 * i, 1);
+    if (warp == 0) *abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+
+  // the ring: lanes 0 and 1 bring a tile each
+  const int step = cs * kWarps;
+  const int32_t *table = a.table + r * a.max_pages;
+  const int tiles_per_page = a.page_size / kTileTokens;
+  const uint64_t policy = policy_evict_first();
+  auto issue = [&](int c, int stage) {
+    const int tile = 2 * (c0 + c) + lane;
+    const bool want = lane < 2 && tile * kTileTokens < hi_max;
+    bool ok = false;
+    int64_t at = 0;
+    if (want) {
+      const int64_t page = table[tile / tiles_per_page];
+      ok = page >= 0 && page < a.pages;
+      if (!ok) set_status(a.dev_status, DSPARK_ERR_PAGES);
+      at = (page * a.Hkv + h) * tiles_per_page + tile % tiles_per_page;
+    }
+    const uint32_t got = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) mbar_arrive_tx(bar + 8 * stage, __popc(got) * tile_bytes(D));
+    __syncwarp();
+    if (ok)
+      bulk_g2s(ring + stage * Sh::kStage + lane * tile_bytes(D), a.cache + at * tile_bytes(D), tile_bytes(D),
+               bar + 8 * stage, policy);
+  };
+  const int w0 = rank * kWarps + warp;
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i)
+    if (w0 + i * step < chunks) issue(w0 + i * step, i);
+
+  // queries: row g of each n-tile, dimensions [q4 D/4, (q4 + 1) D/4)
+  uint32_t qf[Sh::kQShared ? 1 : NT][KS][2];
+  float rs[NT][2];                           // score of rows 2 q4 and 2 q4 + 1 = rs * accumulator, in log2
+  int hi[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int rho = first + 8 * nt + g;
+    float x[D / 4];
+    float top = 0.0f;
+    if (rho < total) {
+      const T *p = reinterpret_cast<const T *>(a.q) + (row0 + rho / a.group) * a.q_row +
+                   (int64_t)(h * a.group + rho % a.group) * a.q_head + q4 * (D / 4);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const Eight<DT> v = reinterpret_cast<const Eight<DT> *>(p)[i];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[8 * i + k] = Elem<DT>::to(v.e[k]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) x[i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // by 2^(8 - e), e the exponent of the row's largest; rows of zeros and of infinities stay as they are
+    const int e = (int)(__float_as_uint(top) >> 23);
+    const int up = e == 0 || e == 255 ? 0 : min(127 + 8 - e, 126);
+    const float f = ldexpf(1.0f, up);
+    const float back = ldexpf(a.scale_log2, -up);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint32_t b0 = pack2(x[4 * s] * f, x[4 * s + 1] * f), b1 = pack2(x[4 * s + 2] * f, x[4 * s + 3] * f);
+      if constexpr (Sh::kQShared) {
+        if (warp == 0) reinterpret_cast<uint2 *>(q_smem)[(nt * KS + s) * 32 + lane] = make_uint2(b0, b1);
+      } else {
+        qf[nt][s][0] = b0;
+        qf[nt][s][1] = b1;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      rs[nt][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * q4 + c));
+      const int j = (first + 8 * nt + 2 * q4 + c) / a.group;
+      hi[nt][c] = first + 8 * nt + 2 * q4 + c >= total ? 0 : (a.causal ? ctx + j + 1 : (int)kv);
+    }
+  }
+  if constexpr (Sh::kQShared) __syncthreads();
+
+  float o[NT][KS][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.0f;
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.0f;
+  }
+
+  int stage = 0;
+  uint32_t phase = 0;
+  bool alive = true;
+  for (int c = w0; c < chunks; c += step) {
+    if (!mbar_wait(bar + 8 * stage, phase, abort)) {
+      if (lane == 0) set_status(a.dev_status, DSPARK_ERR_DEVICE_TIMEOUT);
+      alive = false;
+      break;
+    }
+    const uint32_t buf = ring + stage * Sh::kStage;
+    const int base = (c0 + c) * kChunk;
+    const bool edge = base < lo_max || base + kChunk > hi_min;
+
+    float s[2][NT][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[t][nt][k] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t tile = buf + t * tile_bytes(D);
+      uint32_t ka[D / 32], kb[D / 32], sa[2], sb[2];
+      lds<D / 8>(tile + tile_k(D, g) + q4 * (D / 8), ka);
+      lds<D / 8>(tile + tile_k(D, g + 8) + q4 * (D / 8), kb);
+      if constexpr (D == 128) {
+        const uint32_t x = e4m3x2(lds_u16(tile + tile_ks(D, g, 2 * q4)));
+        const uint32_t y = e4m3x2(lds_u16(tile + tile_ks(D, g + 8, 2 * q4)));
+        sa[0] = __byte_perm(x, x, 0x1010), sa[1] = __byte_perm(x, x, 0x3232);
+        sb[0] = __byte_perm(y, y, 0x1010), sb[1] = __byte_perm(y, y, 0x3232);
+      } else {
+        const uint32_t x = lds_u8(tile + tile_ks(D, g, q4)), y = lds_u8(tile + tile_ks(D, g + 8, q4));
+        sa[0] = e4m3x2(x * 0x101u), sb[0] = e4m3x2(y * 0x101u);
+        sa[1] = sa[0], sb[1] = sb[0];
+      }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t x[4], y[4];
+        e2m1x8(ka[i], x);
+        e2m1x8(kb[i], y);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int ks = 2 * i + u;
+          const uint32_t fa = sa[ks >> 2], fb = sb[ks >> 2];
+          const uint32_t a0 = mul2(x[2 * u], fa), a1 = mul2(y[2 * u], fb), a2 = mul2(x[2 * u + 1], fa),
+                         a3 = mul2(y[2 * u + 1], fb);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (Sh::kQShared) {
+              uint32_t b[2];
+              lds<8>(smem_u32(q_smem) + ((nt * KS + ks) * 32 + lane) * 8, b);
+              mma_f16(s[t][nt], a0, a1, a2, a3, b[0], b[1]);
+            } else {
+              mma_f16(s[t][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+            }
+          }
+        }
+      }
+    }
+
+    // scores, masks, maxima
+    bool rise = false;
+    float top[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        top[nt][k] = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            float &x = s[t][nt][2 * b + k];
+            x *= rs[nt][k];
+            if (edge) {
+              const int tok = base + 16 * t + 8 * b + g;
+              const bool seen = tok < hi[nt][k] && (!a.window || tok >= hi[nt][k] - a.window);
+              x = seen ? x : -INFINITY;
+            }
+            top[nt][k] = fmaxf(top[nt][k], x);
+          }
+        rise |= top[nt][k] > m[nt][k] + kLazy;
+      }
+    }
+    if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float x = top[nt][k];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float up = fmaxf(m[nt][k], x);
+          const float f = m[nt][k] == -INFINITY ? 0.0f : fast_ex2(m[nt][k] - up);
+          m[nt][k] = up;
+          l[nt][k] *= f;
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            o[nt][i][k] *= f;
+            o[nt][i][2 + k] *= f;
+          }
+        }
+      }
+    }
+
+    // probabilities, as the second product's operand
+    uint32_t pb[2][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float z0 = m[nt][0] == -INFINITY ? 0.0f : kLift - m[nt][0];
+      const float z1 = m[nt][1] == -INFINITY ? 0.0f : kLift - m[nt][1];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = fast_ex2(s[t][nt][k] + (k & 1 ? z1 : z0));
+        l[nt][0] += p[0] + p[2];
+        l[nt][1] += p[1] + p[3];
+        pb[t][nt][0] = transpose8x8(pack2(p[0], p[1]));
+        pb[t][nt][1] = transpose8x8(pack2(p[2], p[3]));
+      }
+    }
+
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t tile = buf + t * tile_bytes(D);
+      uint32_t v0[D / 32], v1[D / 32];           // tokens 2 q4, 2 q4 + 1 of the first and the second half
+      lds<D / 8>(tile + tile_v(D, 2 * q4, g), v0);
+      lds<D / 8>(tile + tile_v(D, 8 + 2 * q4, g), v1);
+      const int group = g * (D / 8) / 16;
+      uint32_t f0 = e4m3x2(lds_u16(tile + tile_vs(D, 2 * q4, group)));
+      uint32_t f1 = e4m3x2(lds_u16(tile + tile_vs(D, 8 + 2 * q4, group)));
+      if (edge) {
+        // Tokens outside the tile's range hold nothing (a stale scale may be a NaN): they count 0.  A
+        // scale that is a NaN inside it belongs to the rows that see its token alone, where 0 * NaN
+        // would carry it to the others: it counts 0 too and then marks those rows' outputs.
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t &f = b ? f1 : f0;
+            const int tok = base + 16 * t + 8 * b + 2 * q4 + e;
+            const uint32_t part = e ? f >> 16 : f & 0xffffu;
+            const bool in = tok >= lo_min && tok < hi_max, nan = (part & 0x7fffu) > 0x7c00u;
+            if (!in || nan) f &= e ? 0x0000ffffu : 0xffff0000u;
+            const uint32_t found = __ballot_sync(0xffffffffu, in && nan);
+            if (found) {
+              for (int x = 0; x < 4; ++x) {
+                if (!((found >> (4 * g + x)) & 1)) continue;
+                const int at = base + 16 * t + 8 * b + 2 * x + e;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int k = 0; k < 2; ++k)
+                    if (at < hi[nt][k] && (!a.window || at >= hi[nt][k] - a.window))
+#pragma unroll
+                      for (int i = 0; i < KS; ++i) o[nt][i][k] = o[nt][i][2 + k] = __int_as_float(0x7fffffff);
+              }
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        uint32_t lo0[4], hi0[4], lo1[4], hi1[4];
+        const uint32_t x0 = v0[i], y0 = v0[D / 64 + i], x1 = v1[i], y1 = v1[D / 64 + i];
+        e2m1x8((x0 & 0x0f0f0f0fu) | ((y0 << 4) & 0xf0f0f0f0u), lo0);
+        e2m1x8(((x0 >> 4) & 0x0f0f0f0fu) | (y0 & 0xf0f0f0f0u), hi0);
+        e2m1x8((x1 & 0x0f0f0f0fu) | ((y1 << 4) & 0xf0f0f0f0u), lo1);
+        e2m1x8(((x1 >> 4) & 0x0f0f0f0fu) | (y1 & 0xf0f0f0f0u), hi1);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t a0 = mul2(lo0[b], f0), a1 = mul2(hi0[b], f0), a2 = mul2(lo1[b], f1), a3 = mul2(hi1[b], f1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][4 * i + b], a0, a1, a2, a3, pb[t][nt][0], pb[t][nt][1]);
+        }
+      }
+    }
+    __syncwarp();
+    const int next = c + STAGES * step;
+    if (next < chunks) issue(next, stage);
+    if (++stage == STAGES) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  if (!alive) {   // a wait gave up: the copies still on their way get one more bounded wait each
+    for (int i = 0; i < STAGES; ++i) {
+      const long long t0 = clock64();
+      while (!mbar_try(bar + 8 * stage, phase) && clock64() - t0 < kTimeoutCycles / 8) {
+      }
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+
+  // the CTA's warps meet
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float x = l[nt][k];
+      x += __shfl_xor_sync(0xffffffffu, x, 4);
+      x += __shfl_xor_sync(0xffffffffu, x, 8);
+      x += __shfl_xor_sync(0xffffffffu, x, 16);
+      l[nt][k] = x;
+      if (x != x && m[nt][k] == -INFINITY) m[nt][k] = 0.0f;   // every score was a NaN: so is the result
+      if (g == 0) {
+        warp_m[warp * Sh::kRows + 8 * nt + 2 * q4 + k] = m[nt][k];
+        warp_l[warp * Sh::kRows + 8 * nt + 2 * q4 + k] = x;
+      }
+    }
+  __syncthreads();
+  float *mine = reinterpret_cast<float *>(smem + warp * Sh::kWarpBytes);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int rr = 8 * nt + 2 * q4 + k;
+      float big = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) big = fmaxf(big, warp_m[w * Sh::kRows + rr]);
+      const float f = m[nt][k] == -INFINITY ? 0.0f : fast_ex2(m[nt][k] - big);
+      // a thread's dimensions of a row: chunk g, in order
+#pragma unroll
+      for (int i = 0; i < KS; i += 2) {
+        float4 v = make_float4(o[nt][i][k] * f, o[nt][i][2 + k] * f, o[nt][i + 1][k] * f, o[nt][i + 1][2 + k] * f);
+        *reinterpret_cast<float4 *>(mine + rr * Sh::kOutRow + g * (D / 8) + 2 * i) = v;
+      }
+    }
+  for (int rr = tid; rr < Sh::kRows; rr += kWarps * 32) {
+    float big = -INFINITY, sum = 0.0f;
+    for (int w = 0; w < kWarps; ++w) big = fmaxf(big, warp_m[w * Sh::kRows + rr]);
+    for (int w = 0; w < kWarps; ++w)
+      if (warp_m[w * Sh::kRows + rr] != -INFINITY)
+        sum += warp_l[w * Sh::kRows + rr] * fast_ex2(warp_m[w * Sh::kRows + rr] - big);
+    cta_m[rr] = big;
+    cta_l[rr] = sum;
+  }
+  __syncthreads();
+  constexpr int kVec = Sh::kRows * D / 4;            // float4 pieces of the tile's output
+  float *acc = reinterpret_cast<float *>(smem);      // warp 0's partial becomes the CTA's
+  for (int i = tid; i < kVec; i += kWarps * 32) {
+    const int rr = i / (D / 4), d = 4 * (i % (D / 4));
+    float4 v = *reinterpret_cast<float4 *>(acc + rr * Sh::kOutRow + d);
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 x = *reinterpret_cast<float4 *>(smem + w * Sh::kWarpBytes + (rr * Sh::kOutRow + d) * 4);
+      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    }
+    *reinterpret_cast<float4 *>(acc + rr * Sh::kOutRow + d) = v;
+  }
+
+  // the cluster's CTAs meet: each takes its share of the output from all of them
+  if (cs > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  for (int i = rank * kWarps * 32 + tid; i < kVec; i += cs * kWarps * 32) {
+    const int rr = i / (D / 4), d = 4 * (i % (D / 4)), rho = first + rr;
+    if (rho >= total) continue;
+    float big = -INFINITY, sum = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int b = 0; b < cs; ++b) big = fmaxf(big, *cluster.map_shared_rank(cta_m + rr, b));
+    for (int b = 0; b < cs; ++b) {
+      const float mb = *cluster.map_shared_rank(cta_m + rr, b);
+      if (mb == -INFINITY) continue;
+      const float f = fast_ex2(mb - big);
+      const float4 x = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(acc + rr * Sh::kOutRow + d, b));
+      sum += *cluster.map_shared_rank(cta_l + rr, b) * f;
+      v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y), v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
+    }
+    const float inv = big == -INFINITY ? 0.0f : a.out_scale / sum;
+    const int64_t at = (row0 + rho / a.group) * a.Hq + h * a.group + rho % a.group;
+    T y[4] = {Elem<DT>::from(v.x * inv), Elem<DT>::from(v.y * inv), Elem<DT>::from(v.z * inv),
+              Elem<DT>::from(v.w * inv)};
+    *reinterpret_cast<uint2 *>(reinterpret_cast<T *>(a.out) + at * D + d) = *reinterpret_cast<uint2 *>(y);
+    if (a.lse && d == 0) a.lse[at] = big == -INFINITY ? -INFINITY : kLn2 * (big - kLift) + logf(sum);
+  }
+  if (cs > 1) cluster.sync();                        // no CTA leaves while another reads it
+}
+
+template <int DT, int D, int NT, int STAGES, int MINB>
+cudaError_t launch(const AttendArgs &a, cudaStream_t s, int sms) {
+  using Sh = Shape<D, NT, STAGES>;
+  auto *fn = attend_kernel<DT, D, NT, STAGES, MINB>;
+  cudaError_t e = ensure_dynamic_smem((const void *)fn, Sh::kSmem);
+  if (e != cudaSuccess) return e;
+  const int row_tiles = (a.max_rows * a.group + Sh::kRows - 1) / Sh::kRows;
+  const int64_t units = a.B * a.Hkv * row_tiles, len = a.max_pages * a.page_size;
+  int cs = 1;
+  while (cs < 8 && units * cs < 4LL * MINB * sms && len >= 2LL * cs * kWarps * kChunk) cs *= 2;
+  if (units * cs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * cs));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, a, row_tiles);
+}
+
+template <int DT, int D>
+cudaError_t launch_rows(const AttendArgs &a, cudaStream_t s, int sms) {
+  const int64_t rows = (int64_t)a.max_rows * a.group;
+  if (rows <= 8) return launch<DT, D, 1, 3, 2>(a, s, sms);
+  if (rows <= 16) return launch<DT, D, 2, 3, 2>(a, s, sms);
+  return launch<DT, D, 4, 4, 1>(a, s, sms);
+}
+
+}  // namespace
+
+cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s, int sms) {
+  if (a.dtype == DSPARK_BF16)
+    return a.D == 128 ? launch_rows<DSPARK_BF16, 128>(a, s, sms) : launch_rows<DSPARK_BF16, 64>(a, s, sms);
+  return a.D == 128 ? launch_rows<DSPARK_F16, 128>(a, s, sms) : launch_rows<DSPARK_F16, 64>(a, s, sms);
+}
+
+}  // namespace dspark

@@ -1,0 +1,168 @@
+// Arguments and shared device code of the operators around a ragged verification step: norm and
+// rotation of heads, the paged cache in 4 bits, attention over it and the logits' penalties.
+//
+// The cache.  An element is kept as e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) with one e4m3 scale
+// for 16 dimensions and a power of two for the whole cache.  element * scale has 2 + 4 significant
+// bits and is a multiple of 2^-10 below 2^12, so it is exact in fp16: what the attention multiplies
+// is what the cache holds, with no rounding in between.  The unit of the layout is a tile of 16
+// tokens of one head, 18 D contiguous bytes (keys, values, key scales, value scales), so that one
+// bulk copy brings a tile and every tile of a page is alike whatever the page size.  Keys lie token
+// by token; values lie in 8 chunks of D/8 dimensions with the 8 tokens of a half-tile side by side
+// in each: a thread of the product P V finds its tokens' pieces of one chunk next to each other.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "dspark_internal.cuh"
+
+namespace dspark {
+
+constexpr int kTileTokens = 16;
+
+__host__ __device__ constexpr int tile_bytes(int D) { return 18 * D; }
+__host__ __device__ constexpr int tile_k(int D, int t) { return t * (D / 2); }
+__host__ __device__ constexpr int tile_v(int D, int t, int chunk) {
+  return 8 * D + (D / 16) * (64 * (t >> 3) + 8 * chunk + (t & 7));
+}
+__host__ __device__ constexpr int tile_ks(int D, int t, int c) { return 16 * D + t * (D / 16) + c; }
+__host__ __device__ constexpr int tile_vs(int D, int t, int c) {
+  return 17 * D + (t >> 3) * (D / 2) + 8 * c + (t & 7);
+}
+
+struct HeadsArgs {
+  const void *q, *k, *v;              // [rows, heads, D] with strides in elements
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+  void *q_out, *k_out;                // contiguous [rows, heads, D]
+  const void *q_weight, *k_weight;    // [D] or null
+  const int32_t *positions;           // [rows] or null (append: the rows' places in the cache)
+  const unsigned long long *turns;    // [rot / 2] or null: no rotation
+  int64_t rows;
+  int Hq, Hkv, D, rot, interleaved, dtype;
+  float gain, eps;
+  // append
+  uint8_t *cache;
+  int64_t pages, max_pages, B;
+  int page_size;
+  float k_inv, v_inv;
+  const int32_t *row_off, *kv_len, *table;
+  int32_t *dev_status;
+};
+
+struct CacheReadArgs {
+  const uint8_t *cache;
+  int64_t pages, max_pages, B, rows;
+  int Hkv, D, page_size;
+  const int32_t *row_off, *kv_len, *table;
+  uint8_t *k, *ks, *v, *vs;
+  int32_t *dev_status;
+};
+
+struct AttendArgs {
+  const void *q;                      // [rows, Hq, D] with strides in elements
+  int64_t q_row, q_head;
+  void *out;                          // contiguous [rows, Hq, D]
+  float *lse;                         // [rows, Hq] or null
+  const uint8_t *cache;
+  int64_t pages, max_pages, B, rows;
+  int Hq, Hkv, D, page_size, group, causal, window, max_rows, dtype;
+  float scale_log2, out_scale;        // on q.k in units of log2, on the output
+  const int32_t *row_off, *kv_len, *table;
+  int32_t *dev_status;
+};
+
+struct PenalizeArgs {
+  const void *logits;
+  void *out;                          // may be `logits`
+  int64_t rows, B, V, hist_cap, draft_cap, bias_cap, mask_words;
+  int dtype;
+  const int32_t *row_off, *hist, *hist_len, *prompt_len, *draft_tok, *bias_tok;
+  const uint32_t *mask;
+  const float *repetition, *presence, *frequency, *bias_val;
+  int32_t *dev_status;
+};
+
+cudaError_t launch_norm_rope(const HeadsArgs &a, cudaStream_t s);
+cudaError_t launch_cache_append(const HeadsArgs &a, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheReadArgs &a, cudaStream_t s);
+cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s, int sms);
+cudaError_t launch_penalize(const PenalizeArgs &a, cudaStream_t s);
+
+// The request of a row: the last r with row_off[r] <= row, by one warp, 32 probes a step (three
+// steps for 2048 requests, where halving would take eleven dependent loads).
+__device__ __forceinline__ int64_t request_of_row(const int32_t *row_off, int64_t B, int64_t row, int lane) {
+  int64_t lo = 0, len = B;
+  while (len > 1) {
+    const int64_t step = (len + 31) / 32;
+    const int64_t at = lo + (int64_t)lane * step;
+    const bool below = (int64_t)lane * step < len && row_off[at] <= row;
+    const uint32_t m = __ballot_sync(0xffffffffu, below);
+    const int last = m ? 31 - __clz(m) : 0;
+    const int64_t end = lo + len;
+    lo += (int64_t)last * step;
+    len = end - lo < step ? end - lo : step;
+  }
+  return lo;
+}
+
+// A row's place in the cache.  Returns false for rows past row_off[B] and for inconsistent
+// arguments, which are recorded in the status word.
+struct RowPlace {
+  int64_t pos, tile;   // token position; index of its tile of head 0 in units of tiles
+  int t;               // token in the tile
+};
+__device__ __forceinline__ bool place_row(const int32_t *row_off, const int32_t *kv_len, const int32_t *table, int64_t B,
+                                          int64_t max_pages, int64_t pages, int page_size, int Hkv, int64_t row,
+                                          int lane, int32_t *status, RowPlace *p) {
+  const int64_t r = request_of_row(row_off, B, row, lane);
+  const int64_t a = row_off[r], b = row_off[r + 1];
+  if (row < a || row >= b) {
+    if (row < row_off[B]) set_status(status, DSPARK_ERR_OFFSETS);
+    return false;
+  }
+  const int64_t pos = (int64_t)kv_len[r] - b + row;
+  if (pos < 0 || pos >= max_pages * page_size) {
+    set_status(status, DSPARK_ERR_LENGTHS);
+    return false;
+  }
+  const int64_t page = table[r * max_pages + pos / page_size];
+  if (page < 0 || page >= pages) {
+    set_status(status, DSPARK_ERR_PAGES);
+    return false;
+  }
+  const int slot = (int)(pos % page_size);
+  p->pos = pos;
+  p->tile = page * Hkv * (page_size / kTileTokens) + slot / kTileTokens;
+  p->t = slot % kTileTokens;
+  return true;
+}
+
+// 8 elements of a row as floats, and back.
+template <int DT>
+struct Elem;
+template <>
+struct Elem<DSPARK_BF16> {
+  using T = __nv_bfloat16;
+  static __device__ __forceinline__ float to(T x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ T from(float x) { return __float2bfloat16_rn(x); }
+};
+template <>
+struct Elem<DSPARK_F16> {
+  using T = __half;
+  static __device__ __forceinline__ float to(T x) { return __half2float(x); }
+  static __device__ __forceinline__ T from(float x) { return __float2half_rn(x); }
+};
+template <>
+struct Elem<DSPARK_F32> {
+  using T = float;
+  static __device__ __forceinline__ float to(T x) { return x; }
+  static __device__ __forceinline__ T from(float x) { return x; }
+};
+
+template <int DT>
+struct alignas(16) Eight {
+  typename Elem<DT>::T e[8];
+};
+
+}  // namespace dspark
