@@ -483,7 +483,7 @@ typedef struct {
 
 /* Ragged rows over the cache.  row_off [B+1] int32; kv_len [B] int32, a request's tokens in the
  * cache with this step's rows among them; page_table [B, max_pages] int32 page ids, entries past a
- * request's last page are not read; rows: the rows of the call's tensors, >= row_off[B].
+ * request's last page are not read, max_pages * page_size < 2^31; rows: the rows of the call's tensors, >= row_off[B].
  * Row j of request r is token kv_len[r] - n_r + j, n_r = row_off[r+1] - row_off[r]. */
 typedef struct {
   const int32_t *row_off, *kv_len, *page_table;
@@ -520,10 +520,16 @@ dspark_status dspark_attn_cache_read(const dspark_cache *cache, const dspark_rag
  * (causal: kv_len[r] - n_r + j + 1), and with window > 0 only t >= hi - window.  A row that sees
  * nothing gets 0 and lse -inf.  lse [rows, q_heads] float, optional: log sum exp(scale q.k).
  * max_rows: no request has more rows (sizes the launch; a larger one is DSPARK_ERR_LENGTHS).
- * BF16, F16.  No workspace. */
+ * BF16, F16.
+ * workspace: >= dspark_attn_paged_workspace_bytes(the same arguments) bytes, 256-byte aligned; where that is
+ * 0 (all but few requests with long tables) it may be NULL. */
+size_t dspark_attn_paged_workspace_bytes(int32_t q_heads, const dspark_cache *cache, const dspark_ragged *where,
+                                         int64_t max_rows);
+
 dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t dtype, const dspark_cache *cache,
                                 const dspark_ragged *where, int64_t max_rows, float scale, int32_t causal,
-                                int64_t window, void *out, float *lse, int32_t *dev_status, void *stream);
+                                int64_t window, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                int32_t *dev_status, void *stream);
 
 /* Penalties, biases and masks of the logits' rows. */
 typedef struct {
@@ -543,7 +549,8 @@ typedef struct {
  *   z = logits[i, v];  n > 0 or s: z = z > 0 ? z / repetition : z * repetition;
  *   z -= presence [n > 0] + frequency n;  z += bias of v;  -inf where the mask forbids v
  * in fp32, rounded once.  out may be logits.  F32, BF16; [rows, V] contiguous.  A mask that allows
- * nothing leaves a row of -inf. */
+ * nothing leaves a row of -inf.  A request has at most 2^20 rows (and draft_cap + 1 with draft_tok),
+ * otherwise DSPARK_ERR_OFFSETS. */
 dspark_status dspark_logits_penalize(const void *logits, int32_t dtype, int64_t rows, int64_t V, int64_t B,
                                      const int32_t *row_off, const dspark_penalties *p, void *out,
                                      int32_t *dev_status, void *stream);

@@ -53,7 +53,8 @@ EXPORTED_SYMBOLS = [
     "dspark_schedule_survival", "dspark_schedule_survival_noalloc", "dspark_schedule_capacity",
     "dspark_schedule_topk", "dspark_schedule_threshold", "dspark_verify_workspace_bytes",
     "dspark_verify_ragged", "dspark_verify_markov_workspace_bytes", "dspark_verify_markov",
-    "dspark_attn_norm_rope", "dspark_attn_append", "dspark_attn_cache_read", "dspark_attn_paged",
+    "dspark_attn_norm_rope", "dspark_attn_append", "dspark_attn_cache_read",
+    "dspark_attn_paged_workspace_bytes", "dspark_attn_paged",
     "dspark_logits_penalize", "dspark_status_string", "dspark_check", "dspark_version",
 ]
 

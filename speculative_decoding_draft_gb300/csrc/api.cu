@@ -604,9 +604,11 @@ dspark_status check_cache(const dspark_cache *c) {
   return aligned16(c->data) ? DSPARK_OK : DSPARK_ERR_UNSUPPORTED;
 }
 
-dspark_status check_ragged(const dspark_ragged *t) {
+dspark_status check_ragged(const dspark_ragged *t, int page_size) {
   if (!t || !t->row_off || !t->kv_len || !t->page_table) return DSPARK_ERR_NULL;
-  if (t->B < 1 || t->B > kMaxB || t->rows < 1 || t->rows > kMaxRows || t->max_pages < 1 || t->max_pages > kMaxRows)
+  // token positions are 32-bit inside the kernels
+  if (t->B < 1 || t->B > kMaxB || t->rows < 1 || t->rows > kMaxRows || t->max_pages < 1 ||
+      t->max_pages > kMaxRows / page_size)
     return DSPARK_ERR_DIMS;
   return DSPARK_OK;
 }
@@ -656,7 +658,7 @@ dspark_status dspark_attn_append(const dspark_heads *k, const dspark_heads *v, c
   if (!k || !v || !dev_status || (q != nullptr) != (q_out != nullptr)) return DSPARK_ERR_NULL;
   if (dtype != DSPARK_F32 && dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_DTYPE;
   dspark_status st = check_cache(cache);
-  if (st == DSPARK_OK) st = check_ragged(where);
+  if (st == DSPARK_OK) st = check_ragged(where, cache->page_size);
   if (st == DSPARK_OK) st = check_heads(*k, dtype);
   if (st == DSPARK_OK) st = check_heads(*v, dtype);
   if (st == DSPARK_OK && q) st = check_heads(*q, dtype);
@@ -690,7 +692,7 @@ dspark_status dspark_attn_cache_read(const dspark_cache *cache, const dspark_rag
                                      void *v, void *v_scale, int32_t *dev_status, void *stream) {
   if (!k || !k_scale || !v || !v_scale || !dev_status) return DSPARK_ERR_NULL;
   dspark_status st = check_cache(cache);
-  if (st == DSPARK_OK) st = check_ragged(where);
+  if (st == DSPARK_OK) st = check_ragged(where, cache->page_size);
   if (st != DSPARK_OK) return st;
   if (!aligned16(k) || !aligned16(v)) return DSPARK_ERR_UNSUPPORTED;
   if (!right_device()) return DSPARK_ERR_UNSUPPORTED;
@@ -704,19 +706,35 @@ dspark_status dspark_attn_cache_read(const dspark_cache *cache, const dspark_rag
   return launch_cache_read(a, (cudaStream_t)stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
+static dspark_status check_attend(int32_t q_heads, const dspark_cache *cache, const dspark_ragged *where,
+                                  int64_t max_rows) {
+  dspark_status st = check_cache(cache);
+  if (st == DSPARK_OK) st = check_ragged(where, cache->page_size);
+  if (st != DSPARK_OK) return st;
+  if (q_heads < 1 || q_heads > kMaxHeads || q_heads % cache->kv_heads || max_rows < 1 || max_rows > (1 << 20))
+    return DSPARK_ERR_DIMS;
+  return DSPARK_OK;
+}
+
+size_t dspark_attn_paged_workspace_bytes(int32_t q_heads, const dspark_cache *cache, const dspark_ragged *where,
+                                         int64_t max_rows) {
+  DeviceInfo dev;
+  if (check_attend(q_heads, cache, where, max_rows) != DSPARK_OK || !device_info(&dev)) return 0;
+  return (size_t)attend_workspace_bytes(where->B, cache->kv_heads, q_heads / cache->kv_heads, cache->head_dim,
+                                        where->max_pages * cache->page_size,
+                                        max_rows < where->rows ? max_rows : where->rows, dev.sms);
+}
+
 dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t dtype, const dspark_cache *cache,
                                 const dspark_ragged *where, int64_t max_rows, float scale, int32_t causal,
-                                int64_t window, void *out, float *lse, int32_t *dev_status, void *stream) {
+                                int64_t window, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                int32_t *dev_status, void *stream) {
   if (!q || !out || !dev_status) return DSPARK_ERR_NULL;
   if (dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_DTYPE;
-  dspark_status st = check_cache(cache);
-  if (st == DSPARK_OK) st = check_ragged(where);
+  dspark_status st = check_attend(q_heads, cache, where, max_rows);
   if (st == DSPARK_OK) st = check_heads(*q, dtype);
   if (st != DSPARK_OK) return st;
-  // token positions are 32-bit inside the kernel
-  if (q_heads < 1 || q_heads > kMaxHeads || q_heads % cache->kv_heads || max_rows < 1 || max_rows > (1 << 20) ||
-      !std::isfinite(scale) || window < 0 || window > kMaxRows || where->max_pages * cache->page_size > kMaxRows)
-    return DSPARK_ERR_DIMS;
+  if (!std::isfinite(scale) || window < 0 || window > kMaxRows) return DSPARK_ERR_DIMS;
   if (!aligned16(out)) return DSPARK_ERR_UNSUPPORTED;
   DeviceInfo dev;
   if (!device_info(&dev)) return DSPARK_ERR_CUDA;
@@ -732,7 +750,10 @@ dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t 
   a.dtype = dtype;
   a.scale_log2 = scale * cache->k_scale * kLog2e;
   a.out_scale = cache->v_scale;
+  a.partial = (float *)workspace;
   a.dev_status = dev_status;
+  const int64_t need = attend_workspace_bytes(a.B, a.Hkv, a.group, a.D, a.max_pages * a.page_size, a.max_rows, dev.sms);
+  if (need && (!workspace || !aligned256(workspace) || workspace_bytes < (size_t)need)) return DSPARK_ERR_WORKSPACE;
   return launch_attend(a, (cudaStream_t)stream, dev.sms) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
@@ -744,9 +765,11 @@ dspark_status dspark_logits_penalize(const void *logits, int32_t dtype, int64_t 
     return DSPARK_ERR_NULL;
   if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return DSPARK_ERR_DTYPE;
   if (rows < 1 || rows > kMaxRows || V < 2 || V > kMaxV || B < 1 || B > kMaxB || p->hist_cap < 1 ||
-      (V + 4095) / 4096 * B > kMaxRows || p->hist_cap > kMaxRows || p->bias_cap < 0 || p->bias_cap > 4096 || (p->draft_tok && p->draft_cap < 1))
+      (V + 1023) / 1024 * B > kMaxRows || p->hist_cap > kMaxRows || p->bias_cap < 0 || p->bias_cap > 4096 || (p->draft_tok && p->draft_cap < 1))
     return DSPARK_ERR_DIMS;
-  if (!right_device()) return DSPARK_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return DSPARK_ERR_CUDA;
+  if (dev.major != 10 || dev.minor != 3) return DSPARK_ERR_UNSUPPORTED;
   PenalizeArgs a = {};
   a.logits = logits, a.out = out, a.dtype = dtype, a.rows = rows, a.B = B, a.V = V;
   a.row_off = row_off, a.hist = p->hist, a.hist_len = p->hist_len, a.prompt_len = p->prompt_len;
@@ -755,7 +778,7 @@ dspark_status dspark_logits_penalize(const void *logits, int32_t dtype, int64_t 
   a.mask = (const uint32_t *)p->mask, a.mask_words = (V + 31) / 32;
   a.repetition = p->repetition, a.presence = p->presence, a.frequency = p->frequency;
   a.dev_status = dev_status;
-  return launch_penalize(a, (cudaStream_t)stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  return launch_penalize(a, (cudaStream_t)stream, dev.sms) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // extern "C"

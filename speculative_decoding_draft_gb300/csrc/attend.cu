@@ -35,17 +35,24 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kWarps = 8;
-constexpr int kChunk = 32;            // tokens of a warp's step: two tiles
 constexpr float kLazy = 8.0f;         // how far (log2) a score may pass the running maximum
 constexpr float kLift = 6.0f;         // probabilities are kept 2^kLift up
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same on an accumulator of zeros.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+      "%10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -84,58 +91,58 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return c;
 }
 
+// Plain loads: the compiler may move them among the products, but not over a wait.
 template <int BYTES>
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[BYTES / 4]) {
-  if constexpr (BYTES == 16)
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(addr));
-  else
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+__device__ __forceinline__ void lds(const uint8_t *p, uint32_t (&w)[BYTES / 4]) {
+  if constexpr (BYTES == 16) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
+__device__ __forceinline__ uint32_t lds_u16(const uint8_t *p) { return *reinterpret_cast<const uint16_t *>(p); }
+__device__ __forceinline__ uint32_t lds_u8(const uint8_t *p) { return *p; }
 
 template <int D, int NT, int STAGES>
 struct Shape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kStage = 2 * tile_bytes(D);
+  static constexpr int kTiles = 256 / D;                           // tiles of a warp's step: 64 or 32 tokens
+  static constexpr int kChunk = kTiles * kTileTokens;
+  static constexpr int kStage = kTiles * tile_bytes(D);
   static constexpr int kRing = STAGES * kStage;                    // per warp
   static constexpr int kOutRow = D + 4;                            // floats; padded against bank conflicts
   static constexpr int kOut = kRows * kOutRow * 4;                 // one warp's partial output
   static constexpr int kWarpBytes = (kRing > kOut ? kRing : kOut); // the ring is reused for it
-  static constexpr bool kQShared = NT > 1;                         // query fragments in shared memory
-  static constexpr int kQ = kQShared ? NT * (D / 16) * 32 * 8 : 0;
+  static constexpr bool kQShared = NT > 1;                         // query fragments stay in shared memory
+  static constexpr int kQ = NT * (D / 16) * 32 * 8;
   static constexpr int kBars = kWarps * STAGES * 8;
-  static constexpr int kMl = kWarps * kRows * 8 + kRows * 8;       // maxima and sums of the warps, of the CTA
+  static constexpr int kMl = kWarps * kRows * 8 + kRows * 12;      // maxima and sums of the warps, of the CTA; scales
   static constexpr int kSmem = kWarps * kWarpBytes + kQ + kBars + kMl + 16;
+  static constexpr int kPartial = kRows * (D + 2);                 // floats of a CTA's partial result
 };
 
 template <int DT, int D, int NT, int STAGES, int MINB>
-__global__ void __launch_bounds__(kWarps * 32, MINB) attend_kernel(const __grid_constant__ AttendArgs a, int row_tiles) {
+__global__ void __launch_bounds__(kWarps * 32, MINB)
+    attend_kernel(const __grid_constant__ AttendArgs a, int row_tiles, int parts) {
   using T = typename Elem<DT>::T;
   using Sh = Shape<D, NT, STAGES>;
   constexpr int KS = D / 16;                 // k-steps of q.k, and m-tiles of the output
+  constexpr int TC = Sh::kTiles, kChunk = Sh::kChunk;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *q_smem = smem + kWarps * Sh::kWarpBytes;
   uint64_t *bars = reinterpret_cast<uint64_t *>(q_smem + Sh::kQ);
   float *warp_m = reinterpret_cast<float *>(bars + kWarps * STAGES);
   float *warp_l = warp_m + kWarps * Sh::kRows;
   float *cta_m = warp_l + kWarps * Sh::kRows, *cta_l = cta_m + Sh::kRows;
-  volatile int *abort = reinterpret_cast<volatile int *>(cta_l + Sh::kRows);
+  float *row_scale = cta_l + Sh::kRows;
+  volatile int *abort = reinterpret_cast<volatile int *>(row_scale + Sh::kRows);
 
   cg::cluster_group cluster = cg::this_cluster();
-  const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int cs = (int)cluster.num_blocks(), rank = (int)(blockIdx.x % (unsigned)parts);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
-  int64_t unit = blockIdx.x / cs;
+  int64_t unit = blockIdx.x / (unsigned)parts;
   const int rt = (int)(unit % row_tiles);
   unit /= row_tiles;
   const int h = (int)(unit % a.Hkv);
@@ -175,41 +182,47 @@ __global__ void __launch_bounds__(kWarps * 32, MINB) attend_kernel(const __grid_
   }
   __syncthreads();
 
-  // the ring: lanes 0 and 1 bring a tile each
-  const int step = cs * kWarps;
+  // The ring.  Where a step's tiles always lie in one page, lane 0 brings them with one copy, else one lane
+  // each.  A lane's place moves on by the same number every step, so its page and its place there follow
+  // by an addition; the page's id is looked up a step ahead.
+  const int step = parts * kWarps, w0 = rank * kWarps + warp;
   const int32_t *table = a.table + r * a.max_pages;
   const int tiles_per_page = a.page_size / kTileTokens;
+  const bool whole = tiles_per_page % TC == 0;
+  const int bytes = (whole ? TC : 1) * tile_bytes(D), per_page = whole ? tiles_per_page / TC : tiles_per_page;
+  const int per_step = whole ? 1 : TC;       // pieces of a step
+  const int pieces = lane < per_step ? (whole ? c0 + chunks : (hi_max + kTileTokens - 1) / kTileTokens) : 0;
+  const int ahead = per_step * step, ahead_pages = ahead / per_page, ahead_rest = ahead % per_page;
+  int piece = per_step * (c0 + w0) + lane, page_at = piece / per_page, in_page = piece % per_page;
+  int32_t page = w0 < chunks && piece < pieces ? table[page_at] : -1;
+  const uint8_t *head = a.cache + (int64_t)h * tiles_per_page * tile_bytes(D);
+  const int64_t page_bytes = (int64_t)a.Hkv * tiles_per_page * tile_bytes(D);
   const uint64_t policy = policy_evict_first();
-  auto issue = [&](int c, int stage) {
-    const int tile = 2 * (c0 + c) + lane;
-    const bool want = lane < 2 && tile * kTileTokens < hi_max;
-    bool ok = false;
-    int64_t at = 0;
-    if (want) {
-      const int64_t page = table[tile / tiles_per_page];
-      ok = page >= 0 && page < a.pages;
-      if (!ok) set_status(a.dev_status, DSPARK_ERR_PAGES);
-      at = (page * a.Hkv + h) * tiles_per_page + tile % tiles_per_page;
-    }
+  auto issue = [&](int c, int stage) {       // chunk c, and the look-up for chunk c + step
+    const bool want = piece < pieces, ok = want && page >= 0 && page < a.pages;
+    if (want && !ok) set_status(a.dev_status, DSPARK_ERR_PAGES);
     const uint32_t got = __ballot_sync(0xffffffffu, ok);
-    if (lane == 0) mbar_arrive_tx(bar + 8 * stage, __popc(got) * tile_bytes(D));
+    if (lane == 0) mbar_arrive_tx(bar + 8 * stage, __popc(got) * bytes);
     __syncwarp();
     if (ok)
-      bulk_g2s(ring + stage * Sh::kStage + lane * tile_bytes(D), a.cache + at * tile_bytes(D), tile_bytes(D),
+      bulk_g2s(ring + stage * Sh::kStage + lane * tile_bytes(D), head + page * page_bytes + in_page * bytes, bytes,
                bar + 8 * stage, policy);
+    piece += ahead;
+    page_at += ahead_pages;
+    in_page += ahead_rest;
+    if (in_page >= per_page) {
+      in_page -= per_page;
+      ++page_at;
+    }
+    page = c + step < chunks && piece < pieces ? table[page_at] : -1;
   };
-  const int w0 = rank * kWarps + warp;
 #pragma unroll
   for (int i = 0; i < STAGES; ++i)
     if (w0 + i * step < chunks) issue(w0 + i * step, i);
 
-  // queries: row g of each n-tile, dimensions [q4 D/4, (q4 + 1) D/4)
-  uint32_t qf[Sh::kQShared ? 1 : NT][KS][2];
-  float rs[NT][2];                           // score of rows 2 q4 and 2 q4 + 1 = rs * accumulator, in log2
-  int hi[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int rho = first + 8 * nt + g;
+  // Queries, an n-tile a warp: a lane has row g, dimensions [q4 D/4, (q4 + 1) D/4).
+  if (warp < NT) {
+    const int rho = first + 8 * warp + g;
     float x[D / 4];
     float top = 0.0f;
     if (rho < total) {
@@ -232,61 +245,59 @@ __global__ void __launch_bounds__(kWarps * 32, MINB) attend_kernel(const __grid_
     // by 2^(8 - e), e the exponent of the row's largest; rows of zeros and of infinities stay as they are
     const int e = (int)(__float_as_uint(top) >> 23);
     const int up = e == 0 || e == 255 ? 0 : min(127 + 8 - e, 126);
-    const float f = ldexpf(1.0f, up);
-    const float back = ldexpf(a.scale_log2, -up);
+    const float f = copysignf(ldexpf(1.0f, up), a.scale_log2);   // the scale's sign goes with the queries,
+    if (q4 == 0) row_scale[8 * warp + g] = fmaxf(ldexpf(fabsf(a.scale_log2), -up), 1e-37f);   // so that maxima can
+#pragma unroll                                                                                // be taken unscaled
+    for (int s = 0; s < KS; ++s)
+      reinterpret_cast<uint2 *>(q_smem)[((warp * KS + s) / 2 * 32 + lane) * 2 + (s & 1)] =
+          make_uint2(pack2(x[4 * s] * f, x[4 * s + 1] * f), pack2(x[4 * s + 2] * f, x[4 * s + 3] * f));
+  }
+  __syncthreads();
+  uint32_t qf[Sh::kQShared ? 1 : KS / 2][4];
+  if constexpr (!Sh::kQShared) {
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const uint32_t b0 = pack2(x[4 * s] * f, x[4 * s + 1] * f), b1 = pack2(x[4 * s + 2] * f, x[4 * s + 3] * f);
-      if constexpr (Sh::kQShared) {
-        if (warp == 0) reinterpret_cast<uint2 *>(q_smem)[(nt * KS + s) * 32 + lane] = make_uint2(b0, b1);
-      } else {
-        qf[nt][s][0] = b0;
-        qf[nt][s][1] = b1;
-      }
-    }
+    for (int i = 0; i < KS / 2; ++i) lds<16>(q_smem + (i * 32 + lane) * 16, qf[i]);
+  }
+  float rs[NT][2];                           // score of rows 2 q4 and 2 q4 + 1 = rs * accumulator, in log2; rs > 0
+  int hi[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      rs[nt][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * q4 + c));
-      const int j = (first + 8 * nt + 2 * q4 + c) / a.group;
-      hi[nt][c] = first + 8 * nt + 2 * q4 + c >= total ? 0 : (a.causal ? ctx + j + 1 : (int)kv);
+      const int rr = 8 * nt + 2 * q4 + c, rho = first + rr;
+      rs[nt][c] = row_scale[rr];
+      hi[nt][c] = rho >= total ? 0 : (a.causal ? ctx + rho / a.group + 1 : (int)kv);
     }
-  }
-  if constexpr (Sh::kQShared) __syncthreads();
 
-  float o[NT][KS][4], m[NT][2], l[NT][2];
+  // m: the running maximum in log2, moved when an accumulator passes bar_at; probabilities are 2^(score + z)
+  float o[NT][KS][4], m[NT][2], l[NT][2], z[NT][2], bar_at[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.0f;
-    m[nt][0] = m[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.0f;
+    m[nt][0] = m[nt][1] = bar_at[nt][0] = bar_at[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = z[nt][0] = z[nt][1] = 0.0f;
   }
 
   int stage = 0;
   uint32_t phase = 0;
   bool alive = true;
   for (int c = w0; c < chunks; c += step) {
-    if (!mbar_wait(bar + 8 * stage, phase, abort)) {
+    if (!mbar_try(bar + 8 * stage, phase) && !mbar_wait(bar + 8 * stage, phase, abort)) {
       if (lane == 0) set_status(a.dev_status, DSPARK_ERR_DEVICE_TIMEOUT);
       alive = false;
       break;
     }
-    const uint32_t buf = ring + stage * Sh::kStage;
+    const uint8_t *buf = smem + warp * Sh::kWarpBytes + stage * Sh::kStage;
     const int base = (c0 + c) * kChunk;
     const bool edge = base < lo_max || base + kChunk > hi_min;
 
-    float s[2][NT][4];
+    float s[TC][NT][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[t][nt][k] = 0.0f;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint32_t tile = buf + t * tile_bytes(D);
+    for (int t = 0; t < TC; ++t) {
+      const uint8_t *tile = buf + t * tile_bytes(D);
       uint32_t ka[D / 32], kb[D / 32], sa[2], sb[2];
       lds<D / 8>(tile + tile_k(D, g) + q4 * (D / 8), ka);
       lds<D / 8>(tile + tile_k(D, g + 8) + q4 * (D / 8), kb);
@@ -305,62 +316,67 @@ __global__ void __launch_bounds__(kWarps * 32, MINB) attend_kernel(const __grid_
         uint32_t x[4], y[4];
         e2m1x8(ka[i], x);
         e2m1x8(kb[i], y);
+        const uint32_t fa = sa[i >> 1], fb = sb[i >> 1];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int ks = 2 * i + u;
-          const uint32_t fa = sa[ks >> 2], fb = sb[ks >> 2];
-          const uint32_t a0 = mul2(x[2 * u], fa), a1 = mul2(y[2 * u], fb), a2 = mul2(x[2 * u + 1], fa),
-                         a3 = mul2(y[2 * u + 1], fb);
+        for (int u = 0; u < 4; ++u) x[u] = mul2(x[u], fa), y[u] = mul2(y[u], fb);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (Sh::kQShared) {
-              uint32_t b[2];
-              lds<8>(smem_u32(q_smem) + ((nt * KS + ks) * 32 + lane) * 8, b);
-              mma_f16(s[t][nt], a0, a1, a2, a3, b[0], b[1]);
-            } else {
-              mma_f16(s[t][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
-            }
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t b[4];
+          if constexpr (Sh::kQShared) {
+            lds<16>(q_smem + ((nt * (KS / 2) + i) * 32 + lane) * 16, b);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) b[u] = qf[i][u];
           }
+          if (i == 0)
+            mma_f16_first(s[t][nt], x[0], y[0], x[1], y[1], b[0], b[1]);
+          else
+            mma_f16(s[t][nt], x[0], y[0], x[1], y[1], b[0], b[1]);
+          mma_f16(s[t][nt], x[2], y[2], x[3], y[3], b[2], b[3]);
         }
       }
     }
 
-    // scores, masks, maxima
+    // masks and maxima
     bool rise = false;
     float top[NT][2];
+    if (edge) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        top[nt][k] = -INFINITY;
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < TC; ++t)
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            float &x = s[t][nt][2 * b + k];
-            x *= rs[nt][k];
-            if (edge) {
+            for (int b = 0; b < 2; ++b) {
               const int tok = base + 16 * t + 8 * b + g;
               const bool seen = tok < hi[nt][k] && (!a.window || tok >= hi[nt][k] - a.window);
-              x = seen ? x : -INFINITY;
+              if (!seen) s[t][nt][2 * b + k] = -INFINITY;
             }
-            top[nt][k] = fmaxf(top[nt][k], x);
-          }
-        rise |= top[nt][k] > m[nt][k] + kLazy;
-      }
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        top[nt][k] = fmaxf(s[0][nt][k], s[0][nt][2 + k]);
+#pragma unroll
+        for (int t = 1; t < TC; ++t) top[nt][k] = fmaxf(top[nt][k], fmaxf(s[t][nt][k], s[t][nt][2 + k]));
+        rise |= top[nt][k] > bar_at[nt][k];
+      }
     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float x = top[nt][k];
+          float x = top[nt][k] * rs[nt][k];
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
           const float up = fmaxf(m[nt][k], x);
           const float f = m[nt][k] == -INFINITY ? 0.0f : fast_ex2(m[nt][k] - up);
           m[nt][k] = up;
+          z[nt][k] = up == -INFINITY ? 0.0f : kLift - up;
+          bar_at[nt][k] = (up + kLazy) / rs[nt][k];
           l[nt][k] *= f;
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
@@ -372,26 +388,30 @@ __global__ void __launch_bounds__(kWarps * 32, MINB) attend_kernel(const __grid_
     }
 
     // probabilities, as the second product's operand
-    uint32_t pb[2][NT][2];
+    uint32_t pb[TC][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float z0 = m[nt][0] == -INFINITY ? 0.0f : kLift - m[nt][0];
-      const float z1 = m[nt][1] == -INFINITY ? 0.0f : kLift - m[nt][1];
+      const unsigned long long r2 = f2_pack(rs[nt][0], rs[nt][1]);
+      const unsigned long long z2 = f2_pack(z[nt][0], z[nt][1]);
+      unsigned long long l2 = f2_pack(l[nt][0], l[nt][1]);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float p[4];
+      for (int t = 0; t < TC; ++t) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = fast_ex2(s[t][nt][k] + (k & 1 ? z1 : z0));
-        l[nt][0] += p[0] + p[2];
-        l[nt][1] += p[1] + p[3];
-        pb[t][nt][0] = transpose8x8(pack2(p[0], p[1]));
-        pb[t][nt][1] = transpose8x8(pack2(p[2], p[3]));
+        for (int b = 0; b < 2; ++b) {
+          float p0, p1;
+          f2_unpack(f2_fma(f2_pack(s[t][nt][2 * b], s[t][nt][2 * b + 1]), r2, z2), p0, p1);
+          p0 = fast_ex2(p0);
+          p1 = fast_ex2(p1);
+          l2 = f2_add(l2, f2_pack(p0, p1));
+          pb[t][nt][b] = transpose8x8(pack2(p0, p1));
+        }
       }
+      f2_unpack(l2, l[nt][0], l[nt][1]);
     }
 
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint32_t tile = buf + t * tile_bytes(D);
+    for (int t = 0; t < TC; ++t) {
+      const uint8_t *tile = buf + t * tile_bytes(D);
       uint32_t v0[D / 32], v1[D / 32];           // tokens 2 q4, 2 q4 + 1 of the first and the second half
       lds<D / 8>(tile + tile_v(D, 2 * q4, g), v0);
       lds<D / 8>(tile + tile_v(D, 8 + 2 * q4, g), v1);
@@ -464,6 +484,7 @@ __global__ void __launch_bounds__(kWarps * 32, MINB) attend_kernel(const __grid_
     }
   }
 
+  if (a.partial) grid_dep_launch();
   // the CTA's warps meet
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -521,6 +542,20 @@ __global__ void __launch_bounds__(kWarps * 32, MINB) attend_kernel(const __grid_
     *reinterpret_cast<float4 *>(acc + rr * Sh::kOutRow + d) = v;
   }
 
+  if (a.partial) {                                   // the parts meet in the merging kernel
+    float *part = a.partial + (int64_t)blockIdx.x * Sh::kPartial;
+    __syncthreads();
+    if (tid < Sh::kRows) {
+      part[tid] = cta_m[tid];
+      part[Sh::kRows + tid] = cta_l[tid];
+    }
+    if (chunks > rank * kWarps)
+      for (int i = tid; i < kVec; i += kWarps * 32)
+        reinterpret_cast<float4 *>(part + 2 * Sh::kRows)[i] =
+            *reinterpret_cast<const float4 *>(acc + i / (D / 4) * Sh::kOutRow + 4 * (i % (D / 4)));
+    return;
+  }
+
   // the cluster's CTAs meet: each takes its share of the output from all of them
   if (cs > 1)
     cluster.sync();
@@ -550,45 +585,130 @@ __global__ void __launch_bounds__(kWarps * 32, MINB) attend_kernel(const __grid_
   if (cs > 1) cluster.sync();                        // no CTA leaves while another reads it
 }
 
+// Joins the parts of each row: a warp takes a row.
+template <int DT, int D, int NT>
+__global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ AttendArgs a, int row_tiles, int parts) {
+  using T = typename Elem<DT>::T;
+  constexpr int kRows = 8 * NT, kPartial = kRows * (D + 2), kLanes = D / 4;
+  const int lane = threadIdx.x & 31, d = 4 * lane;
+  const int64_t job = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int rr = (int)(job % kRows);
+  int64_t unit = job / kRows;
+  const float *part = a.partial + unit * parts * kPartial;
+  const int rt = (int)(unit % row_tiles);
+  unit /= row_tiles;
+  const int h = (int)(unit % a.Hkv);
+  const int64_t r = unit / a.Hkv;
+  grid_dep_wait();
+  if (r >= a.B || read_status(a.dev_status)) return;
+  const int64_t row0 = a.row_off[r], n = a.row_off[r + 1] - row0;
+  const int64_t rho = (int64_t)rt * kRows + rr;
+  if (rho >= n * a.group) return;
+  float big = -INFINITY;
+  for (int p = lane; p < parts; p += 32) big = fmaxf(big, part[p * kPartial + rr]);
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
+  float sum = 0.0f;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    // the lanes' factors of 32 parts, handed round
+    float f = 0.0f, m = -INFINITY;
+    if (p0 + lane < parts) {
+      m = part[(p0 + lane) * kPartial + rr];
+      f = m == -INFINITY ? 0.0f : fast_ex2(m - big);
+      if (m != -INFINITY) sum = fmaf(part[(p0 + lane) * kPartial + kRows + rr], f, sum);
+    }
+    const uint32_t used = __ballot_sync(0xffffffffu, m != -INFINITY);
+    for (int p = 0; p < min(32, parts - p0); ++p) {
+      const float g = __shfl_sync(0xffffffffu, f, p);
+      if (!((used >> p) & 1) || lane >= kLanes) continue;
+      const float4 x = *reinterpret_cast<const float4 *>(part + (p0 + p) * kPartial + 2 * kRows + rr * D + d);
+      v.x = fmaf(x.x, g, v.x), v.y = fmaf(x.y, g, v.y), v.z = fmaf(x.z, g, v.z), v.w = fmaf(x.w, g, v.w);
+    }
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+  const float inv = big == -INFINITY ? 0.0f : a.out_scale / sum;
+  const int64_t at = (row0 + rho / a.group) * a.Hq + h * a.group + rho % a.group;
+  if (lane < kLanes) {
+    T y[4] = {Elem<DT>::from(v.x * inv), Elem<DT>::from(v.y * inv), Elem<DT>::from(v.z * inv),
+              Elem<DT>::from(v.w * inv)};
+    *reinterpret_cast<uint2 *>(reinterpret_cast<T *>(a.out) + at * D + d) = *reinterpret_cast<uint2 *>(y);
+  }
+  if (a.lse && lane == 0) a.lse[at] = big == -INFINITY ? -INFINITY : kLn2 * (big - kLift) + logf(sum);
+}
+
+// How a call is cut up.
+struct Plan {
+  int nt, row_tiles, parts;
+  bool split;            // parts meet through the workspace and not in a cluster
+  int64_t units;
+};
+
+Plan plan_of(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int sms) {
+  Plan p = {};
+  const int64_t rows = max_rows * group;
+  p.nt = rows <= 8 ? 1 : 2;
+  p.row_tiles = (int)((rows + 8 * p.nt - 1) / (8 * p.nt));
+  p.units = B * Hkv * p.row_tiles;
+  const int64_t slots = 2 * (int64_t)sms, least = kWarps * (int64_t)(4096 / D);   // tokens that give each warp a step
+  p.parts = 1;
+  while (p.parts < 8 && p.units * p.parts < 2 * slots && len >= 2 * p.parts * least) p.parts *= 2;
+  if (p.parts == 8 && p.units * 8 < slots) {
+    const int64_t want = slots / p.units, most = len / least;
+    const int64_t n = want < most ? want : most;
+    if (n > 8) p.parts = (int)(n < 1024 ? n : 1024), p.split = true;
+  }
+  return p;
+}
+
 template <int DT, int D, int NT, int STAGES, int MINB>
-cudaError_t launch(const AttendArgs &a, cudaStream_t s, int sms) {
+cudaError_t launch(const AttendArgs &a, const Plan &p, cudaStream_t s) {
   using Sh = Shape<D, NT, STAGES>;
   auto *fn = attend_kernel<DT, D, NT, STAGES, MINB>;
   cudaError_t e = ensure_dynamic_smem((const void *)fn, Sh::kSmem);
   if (e != cudaSuccess) return e;
-  const int row_tiles = (a.max_rows * a.group + Sh::kRows - 1) / Sh::kRows;
-  const int64_t units = a.B * a.Hkv * row_tiles, len = a.max_pages * a.page_size;
-  int cs = 1;
-  while (cs < 8 && units * cs < 4LL * MINB * sms && len >= 2LL * cs * kWarps * kChunk) cs *= 2;
-  if (units * cs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (p.units * p.parts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * cs));
+  cfg.gridDim = dim3((unsigned)(p.units * p.parts));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = Sh::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cs;
+  at[0].val.clusterDim.x = p.split ? 1 : p.parts;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, a, row_tiles);
+  e = cudaLaunchKernelEx(&cfg, fn, a, p.row_tiles, p.parts);
+  if (e != cudaSuccess || !p.split) return e;
+  cfg.gridDim = dim3((unsigned)(p.units * NT * 2));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, merge_kernel<DT, D, NT>, a, p.row_tiles, p.parts);
 }
 
 template <int DT, int D>
-cudaError_t launch_rows(const AttendArgs &a, cudaStream_t s, int sms) {
-  const int64_t rows = (int64_t)a.max_rows * a.group;
-  if (rows <= 8) return launch<DT, D, 1, 3, 2>(a, s, sms);
-  if (rows <= 16) return launch<DT, D, 2, 3, 2>(a, s, sms);
-  return launch<DT, D, 4, 4, 1>(a, s, sms);
+cudaError_t launch_rows(const AttendArgs &a, const Plan &p, cudaStream_t s) {
+  return p.nt == 1 ? launch<DT, D, 1, 3, 2>(a, p, s) : launch<DT, D, 2, 2, 2>(a, p, s);
 }
 
 }  // namespace
 
+int64_t attend_workspace_bytes(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int sms) {
+  const Plan p = plan_of(B, Hkv, group, D, len, max_rows, sms);
+  return p.split ? p.units * p.parts * 8 * p.nt * (D + 2) * 4 : 0;
+}
+
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s, int sms) {
+  const Plan p = plan_of(a.B, a.Hkv, a.group, a.D, a.max_pages * a.page_size, a.max_rows, sms);
+  AttendArgs b = a;
+  if (!p.split) b.partial = nullptr;
   if (a.dtype == DSPARK_BF16)
-    return a.D == 128 ? launch_rows<DSPARK_BF16, 128>(a, s, sms) : launch_rows<DSPARK_BF16, 64>(a, s, sms);
-  return a.D == 128 ? launch_rows<DSPARK_F16, 128>(a, s, sms) : launch_rows<DSPARK_F16, 64>(a, s, sms);
+    return a.D == 128 ? launch_rows<DSPARK_BF16, 128>(b, p, s) : launch_rows<DSPARK_BF16, 64>(b, p, s);
+  return a.D == 128 ? launch_rows<DSPARK_F16, 128>(b, p, s) : launch_rows<DSPARK_F16, 64>(b, p, s);
 }
 
 }  // namespace dspark

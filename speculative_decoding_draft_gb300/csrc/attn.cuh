@@ -68,6 +68,7 @@ struct AttendArgs {
   int64_t pages, max_pages, B, rows;
   int Hq, Hkv, D, page_size, group, causal, window, max_rows, dtype;
   float scale_log2, out_scale;        // on q.k in units of log2, on the output
+  float *partial;                     // workspace of the split form
   const int32_t *row_off, *kv_len, *table;
   int32_t *dev_status;
 };
@@ -87,21 +88,22 @@ cudaError_t launch_norm_rope(const HeadsArgs &a, cudaStream_t s);
 cudaError_t launch_cache_append(const HeadsArgs &a, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadArgs &a, cudaStream_t s);
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s, int sms);
-cudaError_t launch_penalize(const PenalizeArgs &a, cudaStream_t s);
+// Bytes of AttendArgs::partial that a call needs; len: tokens that its page table can name.
+int64_t attend_workspace_bytes(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int sms);
+cudaError_t launch_penalize(const PenalizeArgs &a, cudaStream_t s, int sms);
 
 // The request of a row: the last r with row_off[r] <= row, by one warp, 32 probes a step (three
 // steps for 2048 requests, where halving would take eleven dependent loads).
 __device__ __forceinline__ int64_t request_of_row(const int32_t *row_off, int64_t B, int64_t row, int lane) {
-  int64_t lo = 0, len = B;
+  int lo = 0, len = (int)B;
   while (len > 1) {
-    const int64_t step = (len + 31) / 32;
-    const int64_t at = lo + (int64_t)lane * step;
-    const bool below = (int64_t)lane * step < len && row_off[at] <= row;
+    const int step = (len + 31) >> 5, at = lane * step;
+    const bool below = at < len && row_off[lo + at] <= row;
     const uint32_t m = __ballot_sync(0xffffffffu, below);
     const int last = m ? 31 - __clz(m) : 0;
-    const int64_t end = lo + len;
-    lo += (int64_t)last * step;
-    len = end - lo < step ? end - lo : step;
+    const int end = lo + len;
+    lo += last * step;
+    len = min(end - lo, step);
   }
   return lo;
 }
@@ -126,15 +128,16 @@ __device__ __forceinline__ bool place_row(const int32_t *row_off, const int32_t 
     set_status(status, DSPARK_ERR_LENGTHS);
     return false;
   }
-  const int64_t page = table[r * max_pages + pos / page_size];
+  // positions are below 2^31: a 32-bit division, the only one
+  const uint32_t tile = (uint32_t)pos / kTileTokens, per = (uint32_t)page_size / kTileTokens, at = tile / per;
+  const int64_t page = table[r * max_pages + at];
   if (page < 0 || page >= pages) {
     set_status(status, DSPARK_ERR_PAGES);
     return false;
   }
-  const int slot = (int)(pos % page_size);
   p->pos = pos;
-  p->tile = page * Hkv * (page_size / kTileTokens) + slot / kTileTokens;
-  p->t = slot % kTileTokens;
+  p->tile = page * (Hkv * (int64_t)per) + (tile - at * per);
+  p->t = (int)((uint32_t)pos % kTileTokens);
   return true;
 }
 

@@ -56,56 +56,59 @@ def declare(L) -> None:
             ("dspark_attn_norm_rope", [H, H, i64, i32, i32, i32, i32, P, R, P, P, f, P, P, P, P]),
             ("dspark_attn_append", [H, H, H, i32, i32, C, W, P, R, P, P, f, P, P, P]),
             ("dspark_attn_cache_read", [C, W, P, P, P, P, P, P]),
-            ("dspark_attn_paged", [H, i32, i32, C, W, i64, f, i32, i64, P, P, P, P]),
+            ("dspark_attn_paged", [H, i32, i32, C, W, i64, f, i32, i64, P, P, P, ctypes.c_size_t, P, P]),
             ("dspark_logits_penalize", [P, i32, i64, i64, i64, P, ctypes.POINTER(_Penalties), P, P, P])):
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
+    L.dspark_attn_paged_workspace_bytes.argtypes = [i32, C, W, i64]
+    L.dspark_attn_paged_workspace_bytes.restype = ctypes.c_size_t
 
 
 # ---------------------------------------------------------------------------
-# argument checks
+# argument checks.  A call's own time counts where a kernel takes 3 us: the common case is one line of
+# comparisons and what is wrong is found out afterwards.  `dev` is a device index.
 # ---------------------------------------------------------------------------
-def _at(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _like(t, name, dtype, shape, dev):
-    """A contiguous CUDA tensor of this type, shape and device."""
+def _refuse(t, name, dtype, shape, dev):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _like(t, name, dtype, shape, dev) -> int:
+    """The address of a contiguous CUDA tensor of this type, shape and device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
         raise ValueError(f"{name} must be contiguous")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    return t
+    return t.data_ptr()
+
+
+def _maybe(t, name, dtype, shape, dev):
+    return None if t is None else _like(t, name, dtype, shape, dev)
 
 
 def _heads(t, name, dtype, rows, heads, dim, dev) -> _Heads:
     """A [rows, heads, dim] tensor whose last dimension is dense; rows and heads may be strided."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (rows, heads, dim):
-        raise ValueError(f"{name} must have shape {(rows, heads, dim)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (rows, heads, dim) and t.get_device() == dev):
+        _refuse(t, name, dtype, (rows, heads, dim), dev)
     sr, sh, sd = t.stride()
-    unit = 16 // t.element_size()
-    if sd != 1 or (rows > 1 and sr % unit) or (heads > 1 and sh % unit) or t.data_ptr() % 16:
+    unit, at = 4 if dtype is torch.float32 else 8, t.data_ptr()
+    if sd != 1 or (rows > 1 and sr % unit) or (heads > 1 and sh % unit) or at % 16:
         raise ValueError(f"{name} must have a dense last dimension and rows and heads on 16-byte boundaries")
-    return _Heads(t.data_ptr(), sr if rows > 1 else 0, sh if heads > 1 else 0)
+    return _Heads(at, sr if rows > 1 else 0, sh if heads > 1 else 0)
 
 
 def _status(status, dev):
     if status is None:
-        return torch.zeros(1, dtype=torch.int32, device=dev)
-    return _like(status, "status", torch.int32, (1,), dev)
+        return torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
+    _like(status, "status", torch.int32, (1,), dev)
+    return status
 
 
 def _dtype(t, name, allowed) -> int:
@@ -120,16 +123,24 @@ def _ragged(row_off, kv_len, page_table, rows, dev) -> _Ragged:
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages] int32")
     B, width = page_table.shape
-    _like(page_table, "page_table", torch.int32, (B, width), dev)
-    _like(row_off, "row_off", torch.int32, (B + 1,), dev)
-    _like(kv_len, "kv_len", torch.int32, (B,), dev)
-    return _Ragged(row_off.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), B, rows, width)
+    i32 = torch.int32
+    return _Ragged(_like(row_off, "row_off", i32, (B + 1,), dev), _like(kv_len, "kv_len", i32, (B,), dev),
+                   _like(page_table, "page_table", i32, (B, width), dev), B, rows, width)
 
 
-def _result(out, key, shape, dtype, dev):
+def _result(out, key, shape, dtype, like, dev):
+    """out[key], checked, or a new tensor beside `like`."""
     t = None if out is None else out.get(key)
-    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _like(t, f"out[{key!r}]", dtype, tuple(shape),
-                                                                              dev)
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _like(t, f"out[{key!r}]", dtype, shape, dev)
+    return t
+
+
+def _stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 # ---------------------------------------------------------------------------
@@ -184,8 +195,9 @@ class Rope:
         self.inv_freq, self.rotary_dim, self.layout = inv, rotary_dim, layout
         self.gain = own_gain if gain is None else float(gain)
         # turns per position in 64-bit fixed point, wrapped: whole turns say nothing
-        fixed = [round(math.fmod(float(x), 2 * math.pi) / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 for x in inv]
-        self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in fixed], dtype=torch.int64, device=device)
+        turn = inv / (2 * math.pi)
+        turn = turn - turn.round()                     # [-1/2, 1/2]: as a signed 64-bit fraction
+        self.turns = (turn * 2.0 ** 64).clamp(max=2.0 ** 63 - 1024).round().to(torch.int64).to(device)
         self._c = _Rope(self.turns.data_ptr(), rotary_dim, layout == "interleaved", self.gain)
 
 
@@ -202,38 +214,38 @@ def norm_rope(q, k=None, positions=None, rope: Optional[Rope] = None, *, q_weigh
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, D]")
     rows, hq, d = q.shape
-    dev, dt = q.device, q.dtype
+    dev, dt = q.get_device(), q.dtype
     if d < 16 or d > 256 or d % 16:
         raise ValueError(f"head dimension must be a multiple of 16 to 256, got {d}")
     qh, kh, hkv, k_out = _heads(q, "q", dt, rows, hq, d, dev), None, 0, None
-    q_out = _result(out, "q", (rows, hq, d), dt, dev)
+    q_out = _result(out, "q", (rows, hq, d), dt, q, dev)
     if k is not None:
         hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else -1
         kh = _heads(k, "k", dt, rows, hkv, d, dev)
-        k_out = _result(out, "k", (rows, hkv, d), dt, dev)
-    _rope_fits(rope, d, dev)
+        k_out = _result(out, "k", (rows, hkv, d), dt, q, dev)
+    turn = _rope_fits(rope, d, dev)
+    at = None
     if rope is not None or positions is not None:
-        _like(positions, "positions", torch.int32, (rows,), dev)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _like(w, name, dt, (d,), dev)
+        at = _like(positions, "positions", torch.int32, (rows,), dev)
+    wq, wk = _maybe(q_weight, "q_weight", dt, (d,), dev), _maybe(k_weight, "k_weight", dt, (d,), dev)
     status = _status(status, dev)
     if rows:
         _ds._raise(_ds.lib().dspark_attn_norm_rope(
-            qh, kh, rows, hq, hkv, d, code, _at(positions), None if rope is None else rope._c, _at(q_weight),
-            _at(k_weight), eps, _at(q_out), _at(k_out), _at(status), _ds._stream(stream)), "dspark_attn_norm_rope")
+            qh, kh, rows, hq, hkv, d, code, at, turn, wq, wk, eps, q_out.data_ptr(),
+            None if k_out is None else k_out.data_ptr(), status.data_ptr(), _stream(stream, dev)), "dspark_attn_norm_rope")
     return dict(q=q_out, k=k_out, status=status)
 
 
 def _rope_fits(rope, d, dev):
     if rope is None:
-        return
+        return None
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")
     if rope.rotary_dim > d:
         raise ValueError(f"rope turns {rope.rotary_dim} dimensions of heads with {d}")
-    if rope.turns.device != dev:
-        raise ValueError(f"rope must be on {dev}, got {rope.turns.device}")
+    if rope.turns.get_device() != dev:
+        raise ValueError(f"rope must be on cuda:{dev}, got {rope.turns.device}")
+    return rope._c
 
 
 # ---------------------------------------------------------------------------
@@ -259,6 +271,7 @@ class PagedCache:
                 raise ValueError(f"{name} must be a power of two, got {x}")
         self.data, self.page_size, self.k_scale, self.v_scale = data, page_size, float(k_scale), float(v_scale)
         self.pages, self.kv_heads, self.head_dim = data.shape[0], data.shape[1], data.shape[3] // 18
+        self.device = data.get_device()
         self._c = _Cache(data.data_ptr(), self.pages, self.kv_heads, self.head_dim, page_size, k_scale, v_scale)
 
     @classmethod
@@ -289,25 +302,21 @@ def cache_append(cache: PagedCache, k, v, row_off, kv_len, page_table, *, positi
     """
     _is_cache(cache)
     code = _dtype(k, "k", (torch.float32, torch.bfloat16, torch.float16))
-    rows, d, dev, dt = k.shape[0], cache.head_dim, cache.data.device, k.dtype
+    rows, d, dev, dt = k.shape[0], cache.head_dim, cache.device, k.dtype
     kh, vh = _heads(k, "k", dt, rows, cache.kv_heads, d, dev), _heads(v, "v", dt, rows, cache.kv_heads, d, dev)
     where = _ragged(row_off, kv_len, page_table, rows, dev)
-    qh, hq, q_out = None, 0, None
+    qh, hq, q_out, q_at = None, 0, None, None
     if q is not None:
         hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
         qh = _heads(q, "q", dt, rows, hq, d, dev)
-        q_out = _result(out, "q", (rows, hq, d), dt, dev)
-    _rope_fits(rope, d, dev)
-    if positions is not None:
-        _like(positions, "positions", torch.int32, (rows,), dev)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _like(w, name, dt, (d,), dev)
+        q_out = _result(out, "q", (rows, hq, d), dt, q, dev)
+        q_at = q_out.data_ptr()
+    turn, at = _rope_fits(rope, d, dev), _maybe(positions, "positions", torch.int32, (rows,), dev)
+    wq, wk = _maybe(q_weight, "q_weight", dt, (d,), dev), _maybe(k_weight, "k_weight", dt, (d,), dev)
     status = _status(status, dev)
     if rows:
-        _ds._raise(_ds.lib().dspark_attn_append(
-            kh, vh, qh, hq, code, cache._c, where, _at(positions), None if rope is None else rope._c, _at(q_weight),
-            _at(k_weight), eps, _at(q_out), _at(status), _ds._stream(stream)), "dspark_attn_append")
+        _ds._raise(_ds.lib().dspark_attn_append(kh, vh, qh, hq, code, cache._c, where, at, turn, wq, wk, eps, q_at,
+                                                status.data_ptr(), _stream(stream, dev)), "dspark_attn_append")
     return dict(q=q_out, status=status)
 
 
@@ -317,21 +326,23 @@ def cache_read(cache: PagedCache, row_off, kv_len, page_table, rows: int, *, out
     v_scale [rows, Hkv, D/16], float8_e4m3fn and exact; an element's value is element * scale * the cache's scale.
     A request's whole text: row_off over kv_len rows each."""
     _is_cache(cache)
-    dev, h, d = cache.data.device, cache.kv_heads, cache.head_dim
+    dev, h, d = cache.device, cache.kv_heads, cache.head_dim
     where = _ragged(row_off, kv_len, page_table, rows, dev)
     f8 = torch.float8_e4m3fn
-    k, v = (_result(out, key, (rows, h, d), f8, dev) for key in ("k", "v"))
-    ks, vs = (_result(out, key, (rows, h, d // 16), f8, dev) for key in ("k_scale", "v_scale"))
+    k, v = (_result(out, key, (rows, h, d), f8, cache.data, dev) for key in ("k", "v"))
+    ks, vs = (_result(out, key, (rows, h, d // 16), f8, cache.data, dev) for key in ("k_scale", "v_scale"))
     status = _status(status, dev)
     if rows:
-        _ds._raise(_ds.lib().dspark_attn_cache_read(cache._c, where, _at(k), _at(ks), _at(v), _at(vs), _at(status),
-                                                    _ds._stream(stream)), "dspark_attn_cache_read")
+        _ds._raise(_ds.lib().dspark_attn_cache_read(cache._c, where, k.data_ptr(), ks.data_ptr(), v.data_ptr(),
+                                                    vs.data_ptr(), status.data_ptr(), _stream(stream, dev)),
+                   "dspark_attn_cache_read")
     return dict(k=k, k_scale=ks, v=v, v_scale=vs, status=status)
 
 
 def attend_paged(q, cache: PagedCache, row_off, kv_len, page_table, *, scale: Optional[float] = None,
                  causal: bool = True, window: int = 0, max_rows: Optional[int] = None, want_lse: bool = False,
-                 out: Optional[dict] = None, status: Optional[torch.Tensor] = None, stream=None) -> dict:
+                 out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Attention of ragged rows over the cache (C ABI dspark_attn_paged).
 
     q [rows, Hq, D] bfloat16 or float16 (rows and heads may be strided), Hq a multiple of the cache's heads;
@@ -345,7 +356,7 @@ def attend_paged(q, cache: PagedCache, row_off, kv_len, page_table, *, scale: Op
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, D]")
     rows, hq, d = q.shape
-    dev = cache.data.device
+    dev = cache.device
     if hq % cache.kv_heads:
         raise ValueError(f"{hq} query heads are no multiple of {cache.kv_heads} key/value heads")
     qh = _heads(q, "q", q.dtype, rows, hq, cache.head_dim, dev)
@@ -354,14 +365,20 @@ def attend_paged(q, cache: PagedCache, row_off, kv_len, page_table, *, scale: Op
         max_rows = rows
     if max_rows < 1 and rows or window < 0:
         raise ValueError("max_rows must be positive and window not negative")
-    o = _result(out, "out", (rows, hq, d), q.dtype, dev)
-    lse = _result(out, "lse", (rows, hq), torch.float32, dev) if want_lse else None
+    o = _result(out, "out", (rows, hq, d), q.dtype, q, dev)
+    lse = _result(out, "lse", (rows, hq), torch.float32, q, dev) if want_lse else None
     status = _status(status, dev)
     if rows:
-        _ds._raise(_ds.lib().dspark_attn_paged(
+        L = _ds.lib()
+        need, at = L.dspark_attn_paged_workspace_bytes(hq, cache._c, where, max_rows), None
+        if need:
+            workspace = _ds._workspace(need, q.device, workspace)
+            at = workspace.data_ptr()
+        _ds._raise(L.dspark_attn_paged(
             qh, hq, code, cache._c, where, max_rows, 1 / math.sqrt(d) if scale is None else scale, bool(causal),
-            int(window), _at(o), _at(lse), _at(status), _ds._stream(stream)), "dspark_attn_paged")
-    return dict(out=o, lse=lse, status=status)
+            int(window), o.data_ptr(), None if lse is None else lse.data_ptr(), at, workspace.numel() if need else 0,
+            status.data_ptr(), _stream(stream, dev)), "dspark_attn_paged")
+    return dict(out=o, lse=lse, status=status, workspace=workspace)
 
 
 # ---------------------------------------------------------------------------
@@ -382,33 +399,26 @@ def penalize_logits(logits, row_off, hist, hist_len, prompt_len, repetition, pre
     if logits.dim() != 2:
         raise ValueError("logits must be [rows, V]")
     rows, V = logits.shape
-    dev, i32, f32 = logits.device, torch.int32, torch.float32
-    _like(logits, "logits", logits.dtype, (rows, V), dev)
+    dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
+    at = _like(logits, "logits", logits.dtype, (rows, V), dev)
     if not isinstance(hist, torch.Tensor) or hist.dim() != 2:
         raise ValueError("hist must be [B, cap] int32")
     B, cap = hist.shape
-    for t, name, dtype, shape in ((hist, "hist", i32, (B, cap)), (row_off, "row_off", i32, (B + 1,)),
-                                  (hist_len, "hist_len", i32, (B,)), (prompt_len, "prompt_len", i32, (B,)),
-                                  (repetition, "repetition", f32, (B,)), (presence, "presence", f32, (B,)),
-                                  (frequency, "frequency", f32, (B,))):
-        _like(t, name, dtype, shape, dev)
     if (bias_tok is None) != (bias_val is None):
         raise ValueError("bias_tok and bias_val go together")
-    n_draft = n_bias = 0
-    if draft_tok is not None:
-        n_draft = draft_tok.shape[1] if isinstance(draft_tok, torch.Tensor) and draft_tok.dim() == 2 else -1
-        _like(draft_tok, "draft_tok", i32, (B, n_draft), dev)
-    if bias_tok is not None:
-        n_bias = bias_tok.shape[1] if isinstance(bias_tok, torch.Tensor) and bias_tok.dim() == 2 else -1
-        _like(bias_tok, "bias_tok", i32, (B, n_bias), dev)
-        _like(bias_val, "bias_val", f32, (B, n_bias), dev)
-    if mask is not None:
-        _like(mask, "mask", i32, (rows, (V + 31) // 32), dev)
-    o = _result(out, "logits", (rows, V), logits.dtype, dev)
+    n_draft = draft_tok.shape[1] if isinstance(draft_tok, torch.Tensor) and draft_tok.dim() == 2 else 0
+    n_bias = bias_tok.shape[1] if isinstance(bias_tok, torch.Tensor) and bias_tok.dim() == 2 else 0
+    one = (B,)
+    off = _like(row_off, "row_off", i32, (B + 1,), dev)
+    p = _Penalties(_like(hist, "hist", i32, (B, cap), dev), _like(hist_len, "hist_len", i32, one, dev),
+                   _like(prompt_len, "prompt_len", i32, one, dev), _maybe(draft_tok, "draft_tok", i32, (B, n_draft), dev),
+                   _like(repetition, "repetition", f32, one, dev), _like(presence, "presence", f32, one, dev),
+                   _like(frequency, "frequency", f32, one, dev), _maybe(bias_tok, "bias_tok", i32, (B, n_bias), dev),
+                   _maybe(bias_val, "bias_val", f32, (B, n_bias), dev),
+                   _maybe(mask, "mask", i32, (rows, (V + 31) // 32), dev), cap, n_draft, n_bias)
+    o = _result(out, "logits", (rows, V), logits.dtype, logits, dev)
     status = _status(status, dev)
     if rows:
-        p = _Penalties(_at(hist), _at(hist_len), _at(prompt_len), _at(draft_tok), _at(repetition), _at(presence),
-                       _at(frequency), _at(bias_tok), _at(bias_val), _at(mask), cap, n_draft, n_bias)
-        _ds._raise(_ds.lib().dspark_logits_penalize(_at(logits), code, rows, V, B, _at(row_off), p, _at(o), _at(status),
-                                                    _ds._stream(stream)), "dspark_logits_penalize")
+        _ds._raise(_ds.lib().dspark_logits_penalize(at, code, rows, V, B, off, p, o.data_ptr(), status.data_ptr(),
+                                                    _stream(stream, dev)), "dspark_logits_penalize")
     return dict(logits=o, status=status)

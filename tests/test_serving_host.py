@@ -75,7 +75,7 @@ def test_cache_refusals(lib):
     assert read(k=264) == read(c=cache(head_dim=256)) == "UNSUPPORTED"
 
     def attend(q=heads(), hq=4, dtype=1, c=None, w=None, most=1, scale=1.0, window=0, out=ONE):
-        return name(lib.dspark_attn_paged(q, hq, dtype, c or cache(), w or ragged(), most, scale, 1, window, out, None,
+        return name(lib.dspark_attn_paged(q, hq, dtype, c or cache(), w or ragged(), most, scale, 1, window, out, None, None, 0,
                                           ONE, None))
     assert attend(q=None) == attend(out=None) == "NULL"
     assert attend(dtype=0) == "DTYPE"
