@@ -2,9 +2,10 @@
 key/value cache held in 4 bits, attention over it, and the penalties, biases and masks of the logits.
 
 All take the ragged rows of the scheduler and the verification: request r owns rows row_off[r] ..
-row_off[r+1]-1 (``tgt_off``), the last of its kv_len[r] tokens.  As in the rest of the binding, arguments
-are checked and marshalled here and the work runs in the library's CUDA kernels on the current stream;
-nothing is synchronised.  Pass ``status`` (one int32 on the device, see ``check``) to share the error word
+row_off[r+1]-1 (``tgt_off``), the last of its kv_len[r] tokens.  The functions here name the arguments;
+csrc/binding.cpp checks them, allocates outputs and workspaces with torch and calls the C ABI on the
+current stream (a kernel may take 3 us: the same checks in Python took 13 us a call).  Nothing is
+synchronised.  Pass ``status`` (one int32 on the device, see ``check``) to share the error word
 of a step; without it each call makes its own.
 """
 from __future__ import annotations
@@ -16,9 +17,6 @@ from typing import Optional
 import torch
 
 import speculative_decoding_draft_gb300 as _ds
-
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-
 
 class _Heads(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
@@ -65,81 +63,36 @@ def declare(L) -> None:
     L.dspark_attn_paged_workspace_bytes.restype = ctypes.c_size_t
 
 
-# ---------------------------------------------------------------------------
-# argument checks.  A call's own time counts where a kernel takes 3 us: the common case is one line of
-# comparisons and what is wrong is found out afterwards.  `dev` is a device index.
-# ---------------------------------------------------------------------------
-def _refuse(t, name, dtype, shape, dev):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+_binding = None
 
 
-def _like(t, name, dtype, shape, dev) -> int:
-    """The address of a contiguous CUDA tensor of this type, shape and device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
-            and t.is_contiguous()):
-        _refuse(t, name, dtype, shape, dev)
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _native():
+    """The native binding (csrc/binding.cpp), which checks the arguments and calls the loaded library."""
+    global _binding
+    if _binding is None:
+        L = _ds.lib()
+        try:
+            from . import _binding as native
+        except ImportError as e:
+            raise _ds.DsparkUnavailable(f"the native binding is not built ({e}); run "
+                                        "`python -c 'import __graft_entry__ as g; g.build()'`") from None
+        native.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "dspark_attn_norm_rope", "dspark_attn_append", "dspark_attn_cache_read",
+            "dspark_attn_paged_workspace_bytes", "dspark_attn_paged", "dspark_logits_penalize")))
+        _binding = native
+    return _binding
 
 
-def _maybe(t, name, dtype, shape, dev):
-    return None if t is None else _like(t, name, dtype, shape, dev)
+def _done(result, where):
+    """The dict of a call, or the entry point's error."""
+    if type(result) is int:
+        raise _ds.DsparkError(result, where)
+    return result
 
 
-def _heads(t, name, dtype, rows, heads, dim, dev) -> _Heads:
-    """A [rows, heads, dim] tensor whose last dimension is dense; rows and heads may be strided."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (rows, heads, dim) and t.get_device() == dev):
-        _refuse(t, name, dtype, (rows, heads, dim), dev)
-    sr, sh, sd = t.stride()
-    unit, at = 4 if dtype is torch.float32 else 8, t.data_ptr()
-    if sd != 1 or (rows > 1 and sr % unit) or (heads > 1 and sh % unit) or at % 16:
-        raise ValueError(f"{name} must have a dense last dimension and rows and heads on 16-byte boundaries")
-    return _Heads(at, sr if rows > 1 else 0, sh if heads > 1 else 0)
-
-
-def _status(status, dev):
-    if status is None:
-        return torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
-    _like(status, "status", torch.int32, (1,), dev)
-    return status
-
-
-def _dtype(t, name, allowed) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in allowed:
-        raise TypeError(f"{name} must be one of {[str(a) for a in allowed]}, got {t.dtype}")
-    return _DTYPES[t.dtype]
-
-
-def _ragged(row_off, kv_len, page_table, rows, dev) -> _Ragged:
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages] int32")
-    B, width = page_table.shape
-    i32 = torch.int32
-    return _Ragged(_like(row_off, "row_off", i32, (B + 1,), dev), _like(kv_len, "kv_len", i32, (B,), dev),
-                   _like(page_table, "page_table", i32, (B, width), dev), B, rows, width)
-
-
-def _result(out, key, shape, dtype, like, dev):
-    """out[key], checked, or a new tensor beside `like`."""
-    t = None if out is None else out.get(key)
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _like(t, f"out[{key!r}]", dtype, shape, dev)
-    return t
-
-
-def _stream(stream, dev):
+def _raw(stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -199,6 +152,7 @@ class Rope:
         turn = turn - turn.round()                     # [-1/2, 1/2]: as a signed 64-bit fraction
         self.turns = (turn * 2.0 ** 64).clamp(max=2.0 ** 63 - 1024).round().to(torch.int64).to(device)
         self._c = _Rope(self.turns.data_ptr(), rotary_dim, layout == "interleaved", self.gain)
+        self._at, self.device = ctypes.addressof(self._c), self.turns.get_device()
 
 
 def norm_rope(q, k=None, positions=None, rope: Optional[Rope] = None, *, q_weight=None, k_weight=None,
@@ -210,42 +164,17 @@ def norm_rope(q, k=None, positions=None, rope: Optional[Rope] = None, *, q_weigh
     k_weight [D] or None (no norm).  Returns q and k of the inputs' shape, contiguous (``out`` may name the
     inputs themselves where those are contiguous).
     """
-    code = _dtype(q, "q", (torch.float32, torch.bfloat16, torch.float16))
-    if q.dim() != 3:
-        raise ValueError("q must be [rows, heads, D]")
-    rows, hq, d = q.shape
-    dev, dt = q.get_device(), q.dtype
-    if d < 16 or d > 256 or d % 16:
-        raise ValueError(f"head dimension must be a multiple of 16 to 256, got {d}")
-    qh, kh, hkv, k_out = _heads(q, "q", dt, rows, hq, d, dev), None, 0, None
-    q_out = _result(out, "q", (rows, hq, d), dt, q, dev)
-    if k is not None:
-        hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else -1
-        kh = _heads(k, "k", dt, rows, hkv, d, dev)
-        k_out = _result(out, "k", (rows, hkv, d), dt, q, dev)
-    turn = _rope_fits(rope, d, dev)
-    at = None
-    if rope is not None or positions is not None:
-        at = _like(positions, "positions", torch.int32, (rows,), dev)
-    wq, wk = _maybe(q_weight, "q_weight", dt, (d,), dev), _maybe(k_weight, "k_weight", dt, (d,), dev)
-    status = _status(status, dev)
-    if rows:
-        _ds._raise(_ds.lib().dspark_attn_norm_rope(
-            qh, kh, rows, hq, hkv, d, code, at, turn, wq, wk, eps, q_out.data_ptr(),
-            None if k_out is None else k_out.data_ptr(), status.data_ptr(), _stream(stream, dev)), "dspark_attn_norm_rope")
-    return dict(q=q_out, k=k_out, status=status)
+    turn = None if rope is None else _of(rope, Rope, "rope")._at
+    if turn is not None and isinstance(q, torch.Tensor) and rope.device != q.get_device():
+        raise ValueError(f"rope must be on {q.device}, got {rope.turns.device}")
+    return _done(_native().norm_rope(q, k, positions, turn, q_weight, k_weight, eps, out, status, _raw(stream)),
+                 "dspark_attn_norm_rope")
 
 
-def _rope_fits(rope, d, dev):
-    if rope is None:
-        return None
-    if not isinstance(rope, Rope):
-        raise TypeError("rope must be a Rope")
-    if rope.rotary_dim > d:
-        raise ValueError(f"rope turns {rope.rotary_dim} dimensions of heads with {d}")
-    if rope.turns.get_device() != dev:
-        raise ValueError(f"rope must be on cuda:{dev}, got {rope.turns.device}")
-    return rope._c
+def _of(x, kind, name):
+    if not isinstance(x, kind):
+        raise TypeError(f"{name} must be a {kind.__name__}")
+    return x
 
 
 # ---------------------------------------------------------------------------
@@ -273,6 +202,7 @@ class PagedCache:
         self.pages, self.kv_heads, self.head_dim = data.shape[0], data.shape[1], data.shape[3] // 18
         self.device = data.get_device()
         self._c = _Cache(data.data_ptr(), self.pages, self.kv_heads, self.head_dim, page_size, k_scale, v_scale)
+        self._at = ctypes.addressof(self._c)
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, head_dim: int, page_size: int = 64, *, k_scale: float = 1.0,
@@ -286,11 +216,6 @@ class PagedCache:
                    page_size, k_scale=k_scale, v_scale=v_scale)
 
 
-def _is_cache(cache):
-    if not isinstance(cache, PagedCache):
-        raise TypeError("cache must be a PagedCache")
-
-
 def cache_append(cache: PagedCache, k, v, row_off, kv_len, page_table, *, positions=None, rope: Optional[Rope] = None,
                  k_weight=None, q=None, q_weight=None, eps: float = 1e-6, out: Optional[dict] = None,
                  status: Optional[torch.Tensor] = None, stream=None) -> dict:
@@ -300,24 +225,12 @@ def cache_append(cache: PagedCache, k, v, row_off, kv_len, page_table, *, positi
     int32; positions [rows] int32 or None (a row's place in its request); with q [rows, Hq, D] the queries are
     normed and rotated in the same pass and returned as q (contiguous).  Two rows must not name the same place.
     """
-    _is_cache(cache)
-    code = _dtype(k, "k", (torch.float32, torch.bfloat16, torch.float16))
-    rows, d, dev, dt = k.shape[0], cache.head_dim, cache.device, k.dtype
-    kh, vh = _heads(k, "k", dt, rows, cache.kv_heads, d, dev), _heads(v, "v", dt, rows, cache.kv_heads, d, dev)
-    where = _ragged(row_off, kv_len, page_table, rows, dev)
-    qh, hq, q_out, q_at = None, 0, None, None
-    if q is not None:
-        hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
-        qh = _heads(q, "q", dt, rows, hq, d, dev)
-        q_out = _result(out, "q", (rows, hq, d), dt, q, dev)
-        q_at = q_out.data_ptr()
-    turn, at = _rope_fits(rope, d, dev), _maybe(positions, "positions", torch.int32, (rows,), dev)
-    wq, wk = _maybe(q_weight, "q_weight", dt, (d,), dev), _maybe(k_weight, "k_weight", dt, (d,), dev)
-    status = _status(status, dev)
-    if rows:
-        _ds._raise(_ds.lib().dspark_attn_append(kh, vh, qh, hq, code, cache._c, where, at, turn, wq, wk, eps, q_at,
-                                                status.data_ptr(), _stream(stream, dev)), "dspark_attn_append")
-    return dict(q=q_out, status=status)
+    _of(cache, PagedCache, "cache")
+    turn = None if rope is None else _of(rope, Rope, "rope")._at
+    if turn is not None and rope.device != cache.device:
+        raise ValueError(f"rope must be on {cache.data.device}, got {rope.turns.device}")
+    return _done(_native().append(cache._at, cache.device, k, v, row_off, kv_len, page_table, positions, turn, k_weight, q,
+                                  q_weight, eps, out, status, _raw(stream)), "dspark_attn_append")
 
 
 def cache_read(cache: PagedCache, row_off, kv_len, page_table, rows: int, *, out: Optional[dict] = None,
@@ -325,18 +238,9 @@ def cache_read(cache: PagedCache, row_off, kv_len, page_table, rows: int, *, out
     """What the cache holds of the rows' tokens (C ABI dspark_attn_cache_read): k, v [rows, Hkv, D] and k_scale,
     v_scale [rows, Hkv, D/16], float8_e4m3fn and exact; an element's value is element * scale * the cache's scale.
     A request's whole text: row_off over kv_len rows each."""
-    _is_cache(cache)
-    dev, h, d = cache.device, cache.kv_heads, cache.head_dim
-    where = _ragged(row_off, kv_len, page_table, rows, dev)
-    f8 = torch.float8_e4m3fn
-    k, v = (_result(out, key, (rows, h, d), f8, cache.data, dev) for key in ("k", "v"))
-    ks, vs = (_result(out, key, (rows, h, d // 16), f8, cache.data, dev) for key in ("k_scale", "v_scale"))
-    status = _status(status, dev)
-    if rows:
-        _ds._raise(_ds.lib().dspark_attn_cache_read(cache._c, where, k.data_ptr(), ks.data_ptr(), v.data_ptr(),
-                                                    vs.data_ptr(), status.data_ptr(), _stream(stream, dev)),
-                   "dspark_attn_cache_read")
-    return dict(k=k, k_scale=ks, v=v, v_scale=vs, status=status)
+    _of(cache, PagedCache, "cache")
+    return _done(_native().read(cache._at, cache.device, row_off, kv_len, page_table, rows, out, status, _raw(stream)),
+                 "dspark_attn_cache_read")
 
 
 def attend_paged(q, cache: PagedCache, row_off, kv_len, page_table, *, scale: Optional[float] = None,
@@ -351,34 +255,9 @@ def attend_paged(q, cache: PagedCache, row_off, kv_len, page_table, *, scale: Op
     most rows of a request (default: what ``rows`` allows; smaller is faster).  Returns out [rows, Hq, D] and,
     with want_lse, lse [rows, Hq] float32.
     """
-    _is_cache(cache)
-    code = _dtype(q, "q", (torch.bfloat16, torch.float16))
-    if q.dim() != 3:
-        raise ValueError("q must be [rows, heads, D]")
-    rows, hq, d = q.shape
-    dev = cache.device
-    if hq % cache.kv_heads:
-        raise ValueError(f"{hq} query heads are no multiple of {cache.kv_heads} key/value heads")
-    qh = _heads(q, "q", q.dtype, rows, hq, cache.head_dim, dev)
-    where = _ragged(row_off, kv_len, page_table, rows, dev)
-    if max_rows is None:
-        max_rows = rows
-    if max_rows < 1 and rows or window < 0:
-        raise ValueError("max_rows must be positive and window not negative")
-    o = _result(out, "out", (rows, hq, d), q.dtype, q, dev)
-    lse = _result(out, "lse", (rows, hq), torch.float32, q, dev) if want_lse else None
-    status = _status(status, dev)
-    if rows:
-        L = _ds.lib()
-        need, at = L.dspark_attn_paged_workspace_bytes(hq, cache._c, where, max_rows), None
-        if need:
-            workspace = _ds._workspace(need, q.device, workspace)
-            at = workspace.data_ptr()
-        _ds._raise(L.dspark_attn_paged(
-            qh, hq, code, cache._c, where, max_rows, 1 / math.sqrt(d) if scale is None else scale, bool(causal),
-            int(window), o.data_ptr(), None if lse is None else lse.data_ptr(), at, workspace.numel() if need else 0,
-            status.data_ptr(), _stream(stream, dev)), "dspark_attn_paged")
-    return dict(out=o, lse=lse, status=status, workspace=workspace)
+    _of(cache, PagedCache, "cache")
+    return _done(_native().paged(q, cache._at, cache.device, row_off, kv_len, page_table, scale, causal, window, max_rows,
+                                 want_lse, out, workspace, status, _raw(stream)), "dspark_attn_paged")
 
 
 # ---------------------------------------------------------------------------
@@ -395,30 +274,5 @@ def penalize_logits(logits, row_off, hist, hist_len, prompt_len, repetition, pre
     float32; mask int32 [rows, ceil(V/32)], bit v%32 of word v//32 allows token v.  Returns logits (``out`` may
     name the input).
     """
-    code = _dtype(logits, "logits", (torch.float32, torch.bfloat16))
-    if logits.dim() != 2:
-        raise ValueError("logits must be [rows, V]")
-    rows, V = logits.shape
-    dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
-    at = _like(logits, "logits", logits.dtype, (rows, V), dev)
-    if not isinstance(hist, torch.Tensor) or hist.dim() != 2:
-        raise ValueError("hist must be [B, cap] int32")
-    B, cap = hist.shape
-    if (bias_tok is None) != (bias_val is None):
-        raise ValueError("bias_tok and bias_val go together")
-    n_draft = draft_tok.shape[1] if isinstance(draft_tok, torch.Tensor) and draft_tok.dim() == 2 else 0
-    n_bias = bias_tok.shape[1] if isinstance(bias_tok, torch.Tensor) and bias_tok.dim() == 2 else 0
-    one = (B,)
-    off = _like(row_off, "row_off", i32, (B + 1,), dev)
-    p = _Penalties(_like(hist, "hist", i32, (B, cap), dev), _like(hist_len, "hist_len", i32, one, dev),
-                   _like(prompt_len, "prompt_len", i32, one, dev), _maybe(draft_tok, "draft_tok", i32, (B, n_draft), dev),
-                   _like(repetition, "repetition", f32, one, dev), _like(presence, "presence", f32, one, dev),
-                   _like(frequency, "frequency", f32, one, dev), _maybe(bias_tok, "bias_tok", i32, (B, n_bias), dev),
-                   _maybe(bias_val, "bias_val", f32, (B, n_bias), dev),
-                   _maybe(mask, "mask", i32, (rows, (V + 31) // 32), dev), cap, n_draft, n_bias)
-    o = _result(out, "logits", (rows, V), logits.dtype, logits, dev)
-    status = _status(status, dev)
-    if rows:
-        _ds._raise(_ds.lib().dspark_logits_penalize(at, code, rows, V, B, off, p, o.data_ptr(), status.data_ptr(),
-                                                    _stream(stream, dev)), "dspark_logits_penalize")
-    return dict(logits=o, status=status)
+    return _done(_native().penalize(logits, row_off, hist, hist_len, prompt_len, repetition, presence, frequency, draft_tok,
+                                    bias_tok, bias_val, mask, out, status, _raw(stream)), "dspark_logits_penalize")
