@@ -549,7 +549,7 @@ typedef struct {
  *   z = logits[i, v];  n > 0 or s: z = z > 0 ? z / repetition : z * repetition;
  *   z -= presence [n > 0] + frequency n;  z += bias of v;  -inf where the mask forbids v
  * in fp32, rounded once.  out may be logits.  F32, BF16; [rows, V] contiguous.  A mask that allows
- * nothing leaves a row of -inf.  A request has at most 2^20 rows (and draft_cap + 1 with draft_tok),
+ * nothing leaves a row of -inf.  A request has less than 2^20 rows (and draft_cap + 1 with draft_tok),
  * otherwise DSPARK_ERR_OFFSETS. */
 dspark_status dspark_logits_penalize(const void *logits, int32_t dtype, int64_t rows, int64_t V, int64_t B,
                                      const int32_t *row_off, const dspark_penalties *p, void *out,

@@ -20,8 +20,9 @@ namespace dspark {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;                    // 16-byte pieces in flight per thread
-constexpr int64_t kMaxRequestRows = 1 << 20;   // its pieces are counted in 32 bits
+constexpr int kSlice = 4096;                  // most tokens of a slice
+constexpr int kRowsAhead = 2;                 // rows whose loads are in flight together
+constexpr int64_t kMaxRequestRows = (1 << 20) - 1;
 constexpr uint32_t kInPrompt = 0x80000000u;   // a count's top bit
 
 struct Bias {
@@ -30,7 +31,7 @@ struct Bias {
 };
 
 template <int DT, bool MASK>
-__global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constant__ PenalizeArgs a, int slice) {
+__global__ void __launch_bounds__(kThreads, DT == DSPARK_F32 ? 4 : 5) penalize_kernel(const __grid_constant__ PenalizeArgs a, int slice) {
   using T = typename Elem<DT>::T;
   constexpr int N = 16 / sizeof(T);           // elements of a piece
   constexpr uint32_t kAll = (1u << N) - 1;
@@ -41,8 +42,8 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constan
   __shared__ int n_list, n_bias;
   const int tid = threadIdx.x;
   const int slices = (int)((a.V + slice - 1) / slice);
-  const int64_t r = blockIdx.x / slices, v0 = (int64_t)(blockIdx.x - r * slices) * slice;
-  const int width = (int)(a.V - v0 < slice ? a.V - v0 : slice);
+  const int r = (int)(blockIdx.x / (unsigned)slices), V = (int)a.V;      // V <= 2^30, B <= 2^20
+  const int v0 = (int)(blockIdx.x - (unsigned)(r * slices)) * slice, width = min(V - v0, slice);
   const int status = read_status(a.dev_status);
   const int64_t first = a.row_off[r], end = a.row_off[r + 1];
   const int64_t n_hist = a.hist_len[r], n_prompt = a.prompt_len[r];
@@ -63,135 +64,149 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constan
   __syncthreads();
 
   // what the slice's tokens have against them
-  const int32_t *hist = a.hist + r * a.hist_cap;
-  const int32_t *draft = a.draft_tok ? a.draft_tok + r * a.draft_cap : nullptr;
+  const int32_t *hist = a.hist + (int64_t)r * a.hist_cap;
+  const int32_t *draft = a.draft_tok ? a.draft_tok + (int64_t)r * a.draft_cap : nullptr;
   auto mark = [&](int at) {
     const uint32_t bit = 1u << (at & 31);
     if (!(atomicOr(&map[at >> 5], bit) & bit)) list[atomicAdd(&n_list, 1)] = (uint16_t)at;
   };
-  auto count = [&](int64_t i, int32_t tok) {
-    if (tok < 0 || tok >= a.V) {
-      set_status(a.dev_status, DSPARK_ERR_TOKEN_RANGE);
-    } else if (tok >= v0 && tok < v0 + width) {
-      const int at = (int)(tok - v0);
-      if (i < n_prompt)
+  const int told = (int)n_prompt, heard = (int)n_hist;
+  auto count = [&](int i, int32_t tok) {
+    const uint32_t at = (uint32_t)(tok - v0);
+    if (at < (uint32_t)width) {                          // a token of the slice, and so of the vocabulary
+      if (i < told)
         atomicOr(&counts[at], kInPrompt);
       else
         atomicAdd(&counts[at], 1u);
-      mark(at);
+      mark((int)at);
+    } else if ((uint32_t)tok >= (uint32_t)V) {
+      set_status(a.dev_status, DSPARK_ERR_TOKEN_RANGE);
     }
   };
-  for (int64_t i = tid; i < n_hist; i += 4 * kThreads) {
+  for (int i = tid; i < heard; i += 4 * kThreads) {
     int32_t tok[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) tok[u] = i + u * kThreads < n_hist ? hist[i + u * kThreads] : -1;
-#pragma unroll 1
-    for (int u = 0; u < 4 && i + u * kThreads < n_hist; ++u)
-      count(i + u * kThreads, u == 0 ? tok[0] : (u == 1 ? tok[1] : (u == 2 ? tok[2] : tok[3])));
+    for (int u = 0; u < 4; ++u) tok[u] = i < heard - u * kThreads ? hist[i + u * kThreads] : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i < heard - u * kThreads) count(i + u * kThreads, tok[u]);
   }
   if (draft)
     for (int64_t k = tid; k < end - first - 1; k += kThreads) {
       const int32_t tok = draft[k];
-      if (tok < 0 || tok >= a.V)
+      if (tok < 0 || tok >= V)
         set_status(a.dev_status, DSPARK_ERR_TOKEN_RANGE);
       else if (tok >= v0 && tok < v0 + width)
         mark((int)(tok - v0));
     }
   for (int64_t k = tid; k < a.bias_cap; k += kThreads) {
-    const int32_t *tok = a.bias_tok + r * a.bias_cap;
+    const int32_t *tok = a.bias_tok + (int64_t)r * a.bias_cap;
     if (tok[k] < v0 || tok[k] >= v0 + width) continue;   // -1 pads the list
     bool again = false;
     for (int64_t b = 0; b < k; ++b) again |= tok[b] == tok[k];
     if (again) continue;
     float sum = 0.0f;                                    // a token listed twice: its biases add up in their order
     for (int64_t b = k; b < a.bias_cap; ++b)
-      if (tok[b] == tok[k]) sum += a.bias_val[r * a.bias_cap + b];
+      if (tok[b] == tok[k]) sum += a.bias_val[(int64_t)r * a.bias_cap + b];
     biases[atomicAdd(&n_bias, 1)] = Bias{(int32_t)(tok[k] - v0), sum};
     mark((int)(tok[k] - v0));
   }
 
-  // First pass.  Pieces lie on 16-byte boundaries of memory: piece c of a row whose slice starts
-  // `shift` elements past one holds elements c N - shift .. + N - 1; those at the ends go element by
-  // element.  Where input and output lie differently, all do.
+  // First pass.  Pieces lie on 16-byte boundaries of memory; what a row's slice has before its first
+  // boundary and after its last goes element by element, and so does all of it where input and output
+  // lie differently.
   const T minus_inf = Elem<DT>::from(-INFINITY);
   const T *in0 = reinterpret_cast<const T *>(a.logits) + first * a.V + v0;
   T *out0 = reinterpret_cast<T *>(a.out) + first * a.V + v0;
   const bool in_place = a.logits == a.out;
   const bool alike = (((uintptr_t)a.logits ^ (uintptr_t)a.out) & 15u) == 0;
-  const uint32_t pieces = (uint32_t)(width + N - 2) / N + 1;
-  const uint32_t items = MASK || !in_place ? (uint32_t)(end - first) * pieces : 0;
-  for (uint32_t item0 = tid; item0 < items; item0 += kUnroll * kThreads) {
-    uint4 raw[kUnroll];
-    int from[kUnroll];
-    uint32_t row[kUnroll], bar[kUnroll];
-    bool whole[kUnroll];
+  constexpr int kPer = kSlice / N / kThreads;       // pieces of a row's slice for a thread
+  const int n_rows = MASK || !in_place ? (int)(end - first) : 0;
+  const int64_t over = reinterpret_cast<char *>(out0) - reinterpret_cast<const char *>(in0);   // from input to output
+  const T *in = in0;
+  const uint32_t *mask = MASK ? a.mask + first * a.mask_words + (v0 >> 5) : nullptr;   // slices begin at words
+  for (int j0 = 0; j0 < n_rows; j0 += kRowsAhead) {
+    uint4 raw[kRowsAhead][kPer];
+    uint32_t bar[kRowsAhead][kPer];                  // tokens that the mask forbids; ~0: no piece
+    const uint4 *body[kRowsAhead];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t item = item0 + u * kThreads;
-      row[u] = item / pieces;
-      const int shift = (int)(((uintptr_t)(in0 + row[u] * a.V) & 15u) / sizeof(T));
-      from[u] = (int)(item - row[u] * pieces) * N - shift;
-      whole[u] = item < items && alike && from[u] >= 0 && from[u] + N <= width;
-      bar[u] = 0;
-      if (MASK && whole[u]) {
-        const int64_t v = v0 + from[u], w = v >> 5;
-        const int off = (int)(v & 31);
-        const uint32_t *mask = a.mask + (first + row[u]) * a.mask_words + w;
-        const uint32_t lo = __ldg(mask), hi = off + N > 32 ? __ldg(mask + 1) : 0u;
-        bar[u] = ~__funnelshift_r(lo, hi, off) & kAll;
-      }
-    }
+    for (int r = 0; r < kRowsAhead; ++r) {
+      const int before = (int)((0u - (uint32_t)(uintptr_t)in) & 15u) / (int)sizeof(T);
+      const int head = alike && before < width ? before : width, pieces = j0 + r < n_rows ? (width - head) / N : 0;
+      body[r] = reinterpret_cast<const uint4 *>(in + head) + tid;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)      // what the mask empties is not read
-      if (whole[u] && (!MASK || (bar[u] != kAll && !(in_place && bar[u] == 0))))
-        raw[u] = __ldcs(reinterpret_cast<const uint4 *>(in0 + row[u] * a.V + from[u]));
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (!whole[u]) continue;
-      if (MASK) {
-        if (in_place && bar[u] == 0) continue;
-        uint32_t *x = reinterpret_cast<uint32_t *>(&raw[u]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (N == 8) {
-            const uint32_t lo = (bar[u] >> (2 * i)) & 1 ? 0xff80u : x[i] & 0xffffu;
-            x[i] = (bar[u] >> (2 * i + 1)) & 1 ? 0xff800000u | lo : (x[i] & 0xffff0000u) | lo;
-          } else {
-            x[i] = (bar[u] >> i) & 1 ? 0xff800000u : x[i];
+      for (int k = 0; k < kPer; ++k) {
+        const int p = tid + k * kThreads;
+        bar[r][k] = ~0u;
+        if (p < pieces) {
+          bar[r][k] = 0;
+          if (MASK) {
+            const int at = head + p * N, off = at & 31;
+            const uint32_t *m = mask + (at >> 5);
+            bar[r][k] = ~__funnelshift_r(__ldg(m), off + N > 32 ? __ldg(m + 1) : 0u, off) & kAll;
           }
         }
       }
-      *reinterpret_cast<uint4 *>(out0 + row[u] * a.V + from[u]) = raw[u];
+      in += a.V;
+      if (MASK) mask += a.mask_words;
     }
-#pragma unroll 1
-    for (int u = 0; u < kUnroll; ++u) {    // the ends
-      const uint32_t item = item0 + u * kThreads, j = item / pieces;
-      if (item >= items) break;
-      const T *in = in0 + j * a.V;
-      const int at = (int)(item - j * pieces) * N - (int)(((uintptr_t)in & 15u) / sizeof(T));
-      if (alike && at >= 0 && at + N <= width) continue;
-      for (int e = max(at, 0); e < min(at + N, width); ++e) {
-        const bool allowed = !MASK || ((a.mask[(first + j) * a.mask_words + ((v0 + e) >> 5)] >> ((v0 + e) & 31)) & 1);
-        out0[j * a.V + e] = allowed ? in[e] : minus_inf;
+#pragma unroll
+    for (int r = 0; r < kRowsAhead; ++r)             // what the mask empties is not read
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (bar[r][k] != ~0u && (!MASK || (bar[r][k] != kAll && !(in_place && bar[r][k] == 0))))
+          raw[r][k] = __ldcs(body[r] + k * kThreads);
+#pragma unroll
+    for (int r = 0; r < kRowsAhead; ++r) {
+      uint4 *to = reinterpret_cast<uint4 *>(reinterpret_cast<uintptr_t>(body[r]) + over);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const uint32_t b = bar[r][k];
+        if (b == ~0u || (MASK && in_place && b == 0)) continue;
+        if (MASK && b) {
+          uint32_t *x = reinterpret_cast<uint32_t *>(&raw[r][k]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (N == 8) {
+              // the bits of a word's two halves, moved to the top of a byte and spread over two each
+              uint32_t m;
+              asm("prmt.b32 %0, %1, %2, 0xCC88;" : "=r"(m) : "r"((b << 7) >> (2 * i)), "r"((b << 6) >> (2 * i)));
+              x[i] = (x[i] & ~m) | (0xff80ff80u & m);
+            } else {
+              x[i] = (b >> i) & 1 ? 0xff800000u : x[i];
+            }
+          }
+        }
+        to[k * kThreads] = raw[r][k];
       }
+    }
+  }
+  for (int j = tid / 32; j < n_rows; j += kThreads / 32) {      // the rows' ends, a warp a row
+    const T *in = in0 + j * a.V;
+    const int before = (int)((0u - (uint32_t)(uintptr_t)in) & 15u) / (int)sizeof(T);
+    const int head = alike && before < width ? before : width, tail = head + (width - head) / N * N;
+    for (int e = tid % 32; e < head + width - tail; e += 32) {
+      const int at = e < head ? e : tail + e - head;
+      const bool allowed = !MASK || ((a.mask[(first + j) * a.mask_words + ((v0 + at) >> 5)] >> (at & 31)) & 1);
+      out0[j * a.V + at] = allowed ? in[at] : minus_inf;
     }
   }
   __syncthreads();
 
   // second pass: the listed tokens
   const int n = n_list;
-  const int64_t changes = (int64_t)n * (end - first);
-  for (int64_t item = tid; item < changes; item += kThreads) {
-    const int j = (int)(item / n), at = list[item - (int64_t)j * n];
+  const uint32_t changes = (uint32_t)n * (uint32_t)(end - first);       // up to 2^12 * 2^20
+  for (uint32_t item = tid; item < changes; item += kThreads) {
+    const int j = (int)(item / (uint32_t)n), at = list[item - (uint32_t)(j * n)];
     if (MASK && !((a.mask[(first + j) * a.mask_words + ((v0 + at) >> 5)] >> ((v0 + at) & 31)) & 1)) continue;
     T *p = out0 + j * a.V + at;
     float z = Elem<DT>::to(*p);
     uint32_t times = counts[at];
-    const bool told = times & kInPrompt;
+    const bool prompted = times & kInPrompt;
     times &= ~kInPrompt;
     if (draft)
       for (int k = 0; k < j; ++k) times += draft[k] == (int32_t)(v0 + at);
-    if (times || told) z = z > 0.0f ? __fdiv_rn(z, rep) : z * rep;
+    if (times || prompted) z = z > 0.0f ? __fdiv_rn(z, rep) : z * rep;
     if (times) z = z - pre - fre * (float)times;
     for (int b = 0; b < n_bias; ++b)
       if (biases[b].at == at) z += biases[b].sum;
@@ -202,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constan
 template <int DT, bool MASK>
 cudaError_t launch(const PenalizeArgs &a, cudaStream_t s, int sms) {
   // Larger slices read the history less often, smaller ones give a few requests more CTAs.
-  int slice = 8192;
+  int slice = kSlice;
   while (slice > 1024 && a.B * ((a.V + slice - 1) / slice) < 4 * sms) slice /= 2;
   const int64_t bias_slots = a.bias_cap < slice ? a.bias_cap : slice;
   const int smem = slice * 4 + slice / 8 + (int)bias_slots * 8 + slice * 2;

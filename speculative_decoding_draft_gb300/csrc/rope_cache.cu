@@ -13,21 +13,24 @@
 // All arithmetic is in fp32; the queries (and the keys of norm_rope) are rounded once, the keys
 // and values that go to the cache once to 4 bits.
 //
-// A warp takes one row, or one of `parts` equal shares of its heads, by itself: it finds the row's
-// place, computes its cosines and sines once, keeps them in registers and goes over the heads with
-// nothing to wait for but its loads, two of them ahead.  A lane holds 8 neighbouring dimensions of a
-// head (one 16-byte load), a head takes D/8 lanes, and the partner of the half layout lies rot/16
-// lanes away; with every dimension's cosine and signed sine both layouts are x C + partner S.
+// A warp takes one row, or one of `parts` equal shares of its heads, by itself: it brings the heads
+// into a ring of its own with bulk copies, all of a usual row under way at once, finds the row's place
+// and angles meanwhile, keeps cosines and sines in registers and goes over the heads.  A lane holds 8
+// neighbouring dimensions of a head, a head takes D/8 lanes, and the partner of the half layout lies
+// rot/16 lanes away; with every dimension's cosine and signed sine both layouts are x C + partner S.
 // Arithmetic goes in pairs of fp32 (one instruction for two).
 //
-// The issue slots bound it before memory does: rows spread over a CTA's threads, each finding its row
-// and head by division, cost 8800 instructions for a row of 48 heads of 128 dimensions.
+// Bound by the latency of its loads until these are all in flight: with two 16-byte loads a lane ahead
+// in registers the append of 9216 rows with 48 heads of 128 dimensions took 75 us, at 30 % of the
+// memory's rate and 44 % of the issue slots.
 #include "attn.cuh"
 
 namespace dspark {
 namespace {
 
-constexpr int kEnoughWarps = 4096;
+// Ring of a warp and CTAs an SM: the append, with more to compute, wants warps rather than bytes under way.
+constexpr int ring_bytes(bool append) { return append ? 4096 : 6144; }
+constexpr int kEnoughWarps = 2048;
 constexpr int kWarps = 4;          // of a CTA; they share nothing
 
 using Pair = unsigned long long;   // two fp32
@@ -39,22 +42,43 @@ __device__ __forceinline__ float2 floats_of(Pair p) {
   return r;
 }
 
-// 8 elements as four pairs and back.
+// 8 elements as four pairs and back, two elements with one conversion.
 template <int DT>
 __device__ __forceinline__ void to_pairs(const Eight<DT> &v, Pair (&x)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = pair_of(Elem<DT>::to(v.e[2 * i]), Elem<DT>::to(v.e[2 * i + 1]));
-}
-template <int DT>
-__device__ __forceinline__ void store_pairs(void *base, int64_t at, const Pair (&x)[4]) {
-  Eight<DT> v;
+  const uint32_t *u = reinterpret_cast<const uint32_t *>(&v);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = floats_of(x[i]);
-    v.e[2 * i] = Elem<DT>::from(f.x);
-    v.e[2 * i + 1] = Elem<DT>::from(f.y);
+    if constexpr (DT == DSPARK_BF16) {
+      x[i] = pair_of(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+    } else if constexpr (DT == DSPARK_F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
+      x[i] = pair_of(f.x, f.y);
+    } else {
+      x[i] = pair_of(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+    }
   }
-  *reinterpret_cast<Eight<DT> *>(reinterpret_cast<typename Elem<DT>::T *>(base) + at) = v;
+}
+template <int DT>
+__device__ __forceinline__ void store_pairs(void *to, const Pair (&x)[4]) {
+  if constexpr (DT == DSPARK_F32) {
+    ulonglong2 *p = reinterpret_cast<ulonglong2 *>(to);
+    p[0] = make_ulonglong2(x[0], x[1]);
+    p[1] = make_ulonglong2(x[2], x[3]);
+  } else {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = floats_of(x[i]);
+      if constexpr (DT == DSPARK_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+        u[i] = *reinterpret_cast<const uint32_t *>(&h);
+      } else {
+        const __half2 h = __floats2half2_rn(f.x, f.y);
+        u[i] = *reinterpret_cast<const uint32_t *>(&h);
+      }
+    }
+    *reinterpret_cast<uint4 *>(to) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
 }
 template <int DT>
 __device__ __forceinline__ Eight<DT> load8(const void *base, int64_t at) {
@@ -135,37 +159,64 @@ __device__ __forceinline__ uint32_t quantize8(const Pair (&x)[4], float inv, uin
   return codes;
 }
 
-template <int DT, int LANES, bool APPEND>
-__global__ void __launch_bounds__(kWarps * 32, APPEND ? 6 : 8) heads_kernel(const __grid_constant__ HeadsArgs a, int log_parts) {
+template <int DT, int LANES, bool FULL, bool APPEND>   // FULL: D = 8 LANES
+__global__ void __launch_bounds__(kWarps * 32, APPEND ? 8 : 7)
+    heads_kernel(const __grid_constant__ HeadsArgs a, int log_parts) {
   using T = typename Elem<DT>::T;
   constexpr int kBeside = 32 / LANES;        // heads side by side in a warp
+  constexpr int kHeads = 2 * kBeside;        // heads of a chunk: two steps
+  constexpr int kChunkBytes = 512 * (int)sizeof(T), kRingBytes = ring_bytes(APPEND), kStages = kRingBytes / kChunkBytes;
+  __shared__ __align__(128) uint8_t ring_s[kWarps][kRingBytes];
   __shared__ __align__(16) float CS[kWarps][2][LANES * 8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES, D = a.D;
+  __shared__ uint64_t bars[kWarps][kStages];
+  __shared__ int abort[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES, D = FULL ? 8 * LANES : a.D;
   const int64_t job = (int64_t)blockIdx.x * kWarps + warp;
   const int64_t row = job >> log_parts;
   if (row >= a.rows) return;
-  const int h0 = (int)(job - (row << log_parts)) * kBeside + lane / LANES, step = kBeside << log_parts;
-  const bool live = 8 * sub < D;
-  // all loads that wait for nothing, before the first wait
-  const T *qp = reinterpret_cast<const T *>(a.q) + row * a.q_row + h0 * a.q_head + 8 * sub;
-  const int64_t q_step = step * a.q_head;
-  auto fetch = [&](const T *p, bool on) {
-    Eight<DT> v = {};
-    if (on) v = *reinterpret_cast<const Eight<DT> *>(p);
-    return v;
+  const int parts = 1 << log_parts, part = (int)(job - (row << log_parts));
+  const bool live = FULL || 8 * sub < D;
+
+  // The chunks: query heads, key heads, value heads; this warp's are part, part + parts, ...
+  const int n_q = (a.Hq + kHeads - 1) / kHeads, n_k = (a.Hkv + kHeads - 1) / kHeads;
+  const int chunks = n_q + (APPEND ? 2 : 1) * n_k;
+  const uint32_t ring = smem_u32(ring_s[warp]), bar = smem_u32(bars[warp]);
+  if (lane < kStages) mbar_init(bar + 8 * lane, 1);
+  if (lane == 0) abort[warp] = 0;
+  __syncwarp();
+  fence_barrier_init();
+  fence_proxy_async_smem();
+  __syncwarp();
+  const uint32_t head_bytes = D * sizeof(T);
+  const uint64_t policy = policy_evict_first();
+  auto issue = [&](int c, int stage) {
+    const bool is_q = c < n_q, is_k = c < n_q + n_k;
+    const int h0 = (is_q ? c : (is_k ? c - n_q : c - n_q - n_k)) * kHeads;
+    const int n = min(kHeads, (is_q ? a.Hq : a.Hkv) - h0);
+    const int64_t rs = is_q ? a.q_row : (is_k ? a.k_row : a.v_row), hs = is_q ? a.q_head : (is_k ? a.k_head : a.v_head);
+    const T *p = reinterpret_cast<const T *>(is_q ? a.q : (is_k ? a.k : a.v)) + row * rs + h0 * hs;
+    if (lane == 0) mbar_arrive_tx(bar + 8 * stage, n * head_bytes);
+    if (hs == D) {                           // heads without gaps: one copy
+      if (lane == 0) bulk_g2s(ring + stage * kChunkBytes, p, n * head_bytes, bar + 8 * stage, policy);
+    } else {
+      __syncwarp();
+      if (lane < n) bulk_g2s(ring + stage * kChunkBytes + lane * head_bytes, p + lane * hs, head_bytes, bar + 8 * stage, policy);
+    }
   };
-  Eight<DT> raw0 = fetch(qp, live && h0 < a.Hq), raw1 = fetch(qp + q_step, live && h0 + step < a.Hq);
-  Eight<DT> w0 = {};
+  for (int i = 0; i < kStages && part + i * parts < chunks; ++i) issue(part + i * parts, i);
+
+  Eight<DT> w0 = {}, w1 = {};
   if (live && a.q_weight) w0 = load8<DT>(a.q_weight, 8 * sub);
-  if (read_status(a.dev_status)) return;
+  if (live && a.k_weight) w1 = load8<DT>(a.k_weight, 8 * sub);
+  // A failed step, and a row that has no place, does nothing; but no copy may be under way at the end.
   RowPlace place = {};
-  if (APPEND && !place_row(a.row_off, a.kv_len, a.table, a.B, a.max_pages, a.pages, a.page_size, a.Hkv, row, lane,
-                           a.dev_status, &place))
-    return;
+  const bool run = !read_status(a.dev_status) &&
+                   (!APPEND || place_row(a.row_off, a.kv_len, a.table, a.B, a.max_pages, a.pages, a.page_size, a.Hkv, row,
+                                         lane, a.dev_status, &place));
   const int half = a.rot / 2;
   const bool turned = 8 * sub < a.rot;
   Pair c[4], s[4];
-  if (half) {
+  if (half && run) {
     const int64_t pos = (APPEND && !a.positions) ? place.pos : (int64_t)a.positions[row];
     float *C = CS[warp][0], *S = CS[warp][1];
     for (int i = lane; i < half; i += 32) {
@@ -225,70 +276,74 @@ __global__ void __launch_bounds__(kWarps * 32, APPEND ? 6 : 8) heads_kernel(cons
   };
 
   Pair w[4];
-  to_pairs<DT>(w0, w);
-  const T *kp = reinterpret_cast<const T *>(a.k) + row * a.k_row + h0 * a.k_head + 8 * sub;
-  const int64_t k_step = step * a.k_head;
-  T *op = reinterpret_cast<T *>(a.q_out) + (row * a.Hq + h0) * D + 8 * sub;
-  const int out_step = step * D;
-  const int beside = lane / LANES;           // the loops run by the warp's first head, so that all lanes stay in them
-  qp += 2 * q_step;
-  for (int h = h0; h - beside < a.Hq; h += step, op += out_step, qp += q_step) {
-    Pair x[4];
-    to_pairs<DT>(raw0, x);
-    raw0 = raw1;
-    raw1 = fetch(qp, live && h + 2 * step < a.Hq);
-    turn_heads(x, a.q_weight != nullptr, w);
-    if (live && h < a.Hq) store_pairs<DT>(op, 0, x);
-  }
-  if (a.Hkv == 0) return;
-
-  if (a.k_weight) {
-    Eight<DT> v = {};
-    if (live) v = load8<DT>(a.k_weight, 8 * sub);
-    to_pairs<DT>(v, w);
-  }
-  raw0 = fetch(kp, live && h0 < a.Hkv), raw1 = fetch(kp + k_step, live && h0 + step < a.Hkv);
-  kp += 2 * k_step;
-  if (!APPEND) {
-    op = reinterpret_cast<T *>(a.k_out) + (row * a.Hkv + h0) * D + 8 * sub;
-    for (int h = h0; h - beside < a.Hkv; h += step, op += out_step, kp += k_step) {
-      Pair x[4];
-      to_pairs<DT>(raw0, x);
-      raw0 = raw1;
-      raw1 = fetch(kp, live && h + 2 * step < a.Hkv);
-      turn_heads(x, a.k_weight != nullptr, w);
-      if (live && h < a.Hkv) store_pairs<DT>(op, 0, x);
-    }
-    return;
-  }
-  const T *vp = reinterpret_cast<const T *>(a.v) + row * a.v_row + h0 * a.v_head + 8 * sub;
-  const int64_t v_step = step * a.v_head;
-  Eight<DT> v0 = fetch(vp, live && h0 < a.Hkv), v1 = fetch(vp + v_step, live && h0 + step < a.Hkv);
-  vp += 2 * v_step;
-  const int64_t head_bytes = (int64_t)(a.page_size / kTileTokens) * tile_bytes(D), tile_step = step * head_bytes;
+  to_pairs<DT>(part < n_q ? w0 : w1, w);
+  const int beside = lane / LANES;
+  const int64_t tile_step = APPEND ? (int64_t)(a.page_size / kTileTokens) * tile_bytes(D) : 0;
   const int w16 = D / 16, at = 4 * sub, t = place.t;      // the lane's 4 bytes of a head
-  uint8_t *tile = a.cache + place.tile * tile_bytes(D) + h0 * head_bytes;
+  T *const q_to = reinterpret_cast<T *>(a.q_out) + (row * a.Hq + beside) * D + 8 * sub;
+  T *const k_to = APPEND ? nullptr : reinterpret_cast<T *>(a.k_out) + (row * a.Hkv + beside) * D + 8 * sub;
+  uint8_t *const tile = APPEND ? a.cache + place.tile * tile_bytes(D) + beside * tile_step : nullptr;
   const int k_at = tile_k(D, t) + at, v_at = tile_v(D, t, at / w16) + at % w16;
   const int ks_at = tile_ks(D, t, sub >> 1), vs_at = tile_vs(D, t, sub >> 1);
-  for (int h = h0; h - beside < a.Hkv; h += step, kp += k_step, vp += v_step, tile += tile_step) {
-    Pair x[4];
-    uint8_t scale;
-    to_pairs<DT>(raw0, x);
-    raw0 = raw1;
-    raw1 = fetch(kp, live && h + 2 * step < a.Hkv);
-    turn_heads(x, a.k_weight != nullptr, w);
-    uint32_t codes = quantize8<DT == DSPARK_F32>(x, a.k_inv, &scale);
-    if (live && h < a.Hkv) {
-      *reinterpret_cast<uint32_t *>(tile + k_at) = codes;
-      if (!(sub & 1)) tile[ks_at] = scale;
+  const uint8_t *const mine = ring_s[warp] + (beside * D + 8 * sub) * sizeof(T);
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int c = part; c < chunks; c += parts) {
+    if (!mbar_try(bar + 8 * stage, phase) && !mbar_wait(bar + 8 * stage, phase, &abort[warp])) {
+      if (lane == 0) set_status(a.dev_status, DSPARK_ERR_DEVICE_TIMEOUT);
+      for (int i = 0; i < kStages && c < chunks; ++i, c += parts) {   // copies on their way get one more bounded wait
+        const long long t0 = clock64();
+        while (!mbar_try(bar + 8 * stage, phase) && clock64() - t0 < kTimeoutCycles / 8) {
+        }
+        if (++stage == kStages) stage = 0, phase ^= 1;
+      }
+      return;
     }
-    to_pairs<DT>(v0, x);
-    v0 = v1;
-    v1 = fetch(vp, live && h + 2 * step < a.Hkv);
-    codes = quantize8<DT == DSPARK_F32>(x, a.v_inv, &scale);
-    if (live && h < a.Hkv) {
-      *reinterpret_cast<uint32_t *>(tile + v_at) = codes;
-      if (!(sub & 1)) tile[vs_at] = scale;
+    Pair x[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      Eight<DT> v = {};
+      if (live) v = *reinterpret_cast<const Eight<DT> *>(mine + stage * kChunkBytes + i * kBeside * D * sizeof(T));
+      to_pairs<DT>(v, x[i]);
+    }
+    __syncwarp();
+    if (c + kStages * parts < chunks) issue(c + kStages * parts, stage);
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    if (!run) continue;
+    if (c < n_q) {
+      const int h0 = c * kHeads, left = a.Hq - h0 - beside;
+      turn_heads(x[0], a.q_weight != nullptr, w);
+      turn_heads(x[1], a.q_weight != nullptr, w);
+      T *to = q_to + h0 * D;
+      if (live && left > 0) store_pairs<DT>(to, x[0]);
+      if (live && left > kBeside) store_pairs<DT>(to + kBeside * D, x[1]);
+      if (c + parts >= n_q) to_pairs<DT>(w1, w);           // the next chunk holds keys
+      continue;
+    }
+    const bool is_v = c >= n_q + n_k;
+    const int h0 = (is_v ? c - n_q - n_k : c - n_q) * kHeads, left = a.Hkv - h0 - beside;
+    if (!is_v) {
+      turn_heads(x[0], a.k_weight != nullptr, w);
+      turn_heads(x[1], a.k_weight != nullptr, w);
+    }
+    if (!APPEND) {
+      T *to = k_to + h0 * D;
+      if (live && left > 0) store_pairs<DT>(to, x[0]);
+      if (live && left > kBeside) store_pairs<DT>(to + kBeside * D, x[1]);
+      continue;
+    }
+    uint8_t *to = tile + h0 * tile_step;
+#pragma unroll
+    for (int i = 0; i < 2; ++i, to += kBeside * tile_step) {
+      uint8_t scale;
+      const uint32_t codes = quantize8<DT == DSPARK_F32>(x[i], is_v ? a.v_inv : a.k_inv, &scale);
+      if (live && left > i * kBeside) {
+        *reinterpret_cast<uint32_t *>(to + (is_v ? v_at : k_at)) = codes;
+        if (!(sub & 1)) to[is_v ? vs_at : ks_at] = scale;
+      }
     }
   }
 }
@@ -300,7 +355,7 @@ __device__ __forceinline__ uint32_t e2m1_to_e4m3(uint32_t c) {
   return mag | sgn;
 }
 
-__global__ void __launch_bounds__(kWarps * 32) read_kernel(const __grid_constant__ CacheReadArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 16) read_kernel(const __grid_constant__ CacheReadArgs a) {
   if (read_status(a.dev_status)) return;
   const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -333,10 +388,14 @@ cudaError_t launch_lanes(const HeadsArgs &a, cudaStream_t s) {
   // a row's heads in shares as long as the rows alone leave the SMs without work: 24 warps on each of
   // 152 and several rounds of them
   int log_parts = 0;
-  const int most = ((a.Hq > a.Hkv ? a.Hq : a.Hkv) * LANES + 31) / 32;
+  const int most = (a.Hq + (APPEND ? 2 : 1) * a.Hkv) * LANES / 64;      // chunks
   while ((a.rows << log_parts) < kEnoughWarps && 2 << log_parts <= most) ++log_parts;
   const int64_t jobs = a.rows << log_parts;
-  heads_kernel<DT, LANES, APPEND><<<(unsigned)((jobs + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(a, log_parts);
+  const unsigned grid = (unsigned)((jobs + kWarps - 1) / kWarps);
+  if (a.D == 8 * LANES)
+    heads_kernel<DT, LANES, true, APPEND><<<grid, kWarps * 32, 0, s>>>(a, log_parts);
+  else
+    heads_kernel<DT, LANES, false, APPEND><<<grid, kWarps * 32, 0, s>>>(a, log_parts);
   return cudaGetLastError();
 }
 
