@@ -4,8 +4,8 @@
 // over the tokens t that a row sees: t < hi, hi = kv_len (causal: kv_len - n + j + 1 for row j of n),
 // and t >= hi - window with a window.  A row that sees nothing gets 0 and lse = -inf.
 //
-// One pass over the cache.  A warp takes 32 tokens (two tiles) at a time, brought by bulk copies into
-// a ring of its own, and works transposed: S^T = K Q^T and O^T = V^T P^T with m16n8k16 products, so
+// One pass over the cache.  A warp takes 32 tokens (64 of heads with 64 dimensions) at a time, brought by
+// bulk copies into a ring of its own, and works transposed: S^T = K Q^T and O^T = V^T P^T with m16n8k16 products, so
 // the tokens (then the dimensions) fill the 16-wide side and the 8-wide side holds the rows: the
 // query heads of one key/value head times the request's rows, 8 for plain decoding with up to 8
 // heads a group, with nothing padded to 16, 64 or 128.  The 4-bit operands go straight from shared
@@ -23,8 +23,24 @@
 // (they are kept 2^6 up so that small ones stay normal fp16 numbers), the result is the same, and the
 // reductions over lanes and the rescaling of the output leave the common path.
 //
-// The tokens of one (request, key/value head, row tile) are dealt to the warps of a cluster of CTAs;
-// partial results meet in shared memory, first of the CTA, then across the cluster.
+// The tokens of one (request, key/value head, row tile) are dealt to the warps of a CTA, of a cluster of
+// CTAs where there are too few units to fill the SMs, or of many CTAs that meet through a workspace where
+// eight still are; partial results meet in shared memory, across the cluster, or in merge_kernel.  Requests
+// start longest first.
+//
+// Measured (one GB300): 64 requests of 512 to 4096 tokens with 1 to 8 rows, 32 query and 8 key/value heads
+// of 128 dimensions 85 us (26 us of reading at the memory's rate); one request of 131071 tokens with 8 rows
+// 87 us (22); 256 requests of up to 16384 tokens, heads of 64 dimensions, 266 us (202).  Bound by the issue
+// slots: a warp's step of 32 tokens by 16 rows is 760 instructions, 136 of them conversions and 128 scalings,
+// both at half rate, and 64 products; the SMs issue 2 a cycle.  Tried and slower or no faster: 32 rows a warp
+// (8 warps an SM: 158 us for the 64 requests), 8 rows (104), two warps sharing a step of 32 rows with half of
+// the output each (133; one request: 85), chunks drawn from a counter instead of dealt (also not
+// reproducible), 24 warps an SM.  The fifth-generation tensor cores take operands from shared or tensor
+// memory only, where every expanded element would have to be written and read again: 1 KB a token and head
+// each way against the 144 bytes that are stored, 3 times what shared memory can move in the time that the
+// stored bytes take to arrive.
+#include <type_traits>
+
 #include <cooperative_groups.h>
 
 #include "attn.cuh"
@@ -34,7 +50,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+constexpr int kCtas = 4;              // on an SM together
 constexpr float kLazy = 8.0f;         // how far (log2) a score may pass the running maximum
 constexpr float kLift = 6.0f;         // probabilities are kept 2^kLift up
 
@@ -105,6 +122,34 @@ __device__ __forceinline__ void lds(const uint8_t *p, uint32_t (&w)[BYTES / 4]) 
 __device__ __forceinline__ uint32_t lds_u16(const uint8_t *p) { return *reinterpret_cast<const uint16_t *>(p); }
 __device__ __forceinline__ uint32_t lds_u8(const uint8_t *p) { return *p; }
 
+// The i-th request, long ones first: CTAs start in the order of their index, and one that starts last must
+// not be the longest.  Eight classes by length; every warp works it out by itself from the lengths, as
+// long as it can hold these (B <= 256; with more requests the last CTAs weigh little).
+constexpr int kOrderMost = 256;
+__device__ __forceinline__ int64_t longest_first(const int32_t *kv_len, int64_t B, int64_t i, int lane) {
+  if (B > kOrderMost || B < 2) return i;
+  int len[kOrderMost / 32], most = 1;
+#pragma unroll
+  for (int j = 0; j < kOrderMost / 32; ++j) {
+    len[j] = 32 * j + lane < B ? max(kv_len[32 * j + lane], 0) : -1;
+    most = max(most, len[j]);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  const float scale = 7.999f / (float)most;
+  int left = (int)i;
+  for (int c = 7; c >= 0; --c) {
+#pragma unroll
+    for (int j = 0; j < kOrderMost / 32; ++j) {
+      if (32 * j >= B) break;
+      const uint32_t in = __ballot_sync(0xffffffffu, len[j] >= 0 && (int)((float)len[j] * scale) == c);
+      const int n = __popc(in);
+      if (left < n) return 32 * j + __fns(in, 0, left + 1);
+      left -= n;
+    }
+  }
+  return i;                                  // not reached
+}
+
 template <int D, int NT, int STAGES>
 struct Shape {
   static constexpr int kRows = 8 * NT;
@@ -119,7 +164,8 @@ struct Shape {
   static constexpr int kQ = NT * (D / 16) * 32 * 8;
   static constexpr int kBars = kWarps * STAGES * 8;
   static constexpr int kMl = kWarps * kRows * 8 + kRows * 12;      // maxima and sums of the warps, of the CTA; scales
-  static constexpr int kSmem = kWarps * kWarpBytes + kQ + kBars + kMl + 16;
+  static constexpr int kPlaces = kWarps * kTiles * 16 + 48;        // the ring's places, see below
+  static constexpr int kSmem = kWarps * kWarpBytes + kQ + kBars + kPlaces + kMl + 16;
   static constexpr int kPartial = kRows * (D + 2);                 // floats of a CTA's partial result
 };
 
@@ -133,7 +179,8 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *q_smem = smem + kWarps * Sh::kWarpBytes;
   uint64_t *bars = reinterpret_cast<uint64_t *>(q_smem + Sh::kQ);
-  float *warp_m = reinterpret_cast<float *>(bars + kWarps * STAGES);
+  int4 *places = reinterpret_cast<int4 *>(bars + kWarps * STAGES), *fixed = places + kWarps * TC;
+  float *warp_m = reinterpret_cast<float *>(fixed + 3);
   float *warp_l = warp_m + kWarps * Sh::kRows;
   float *cta_m = warp_l + kWarps * Sh::kRows, *cta_l = cta_m + Sh::kRows;
   float *row_scale = cta_l + Sh::kRows;
@@ -142,11 +189,13 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = (int)cluster.num_blocks(), rank = (int)(blockIdx.x % (unsigned)parts);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
+  grid_dep_launch();
+  grid_dep_wait();
   int64_t unit = blockIdx.x / (unsigned)parts;
   const int rt = (int)(unit % row_tiles);
   unit /= row_tiles;
   const int h = (int)(unit % a.Hkv);
-  const int64_t r = unit / a.Hkv;
+  const int64_t r = longest_first(a.kv_len, a.B, unit / a.Hkv, lane);
   const int64_t row0 = a.row_off[r], row1 = a.row_off[r + 1], kv = a.kv_len[r];
   const int64_t n = row1 - row0;
   // every CTA of a cluster takes the same way out here
@@ -183,38 +232,53 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
   __syncthreads();
 
   // The ring.  Where a step's tiles always lie in one page, lane 0 brings them with one copy, else one lane
-  // each.  A lane's place moves on by the same number every step, so its page and its place there follow
-  // by an addition; the page's id is looked up a step ahead.
+  // each.  A lane's place (piece, page, piece in the page) moves on by the same numbers every step, so it
+  // follows by an addition; the page's id is looked up a step ahead.  Places and numbers live in shared
+  // memory: registers are what the loop below is short of.
   const int step = parts * kWarps, w0 = rank * kWarps + warp;
   const int32_t *table = a.table + r * a.max_pages;
   const int tiles_per_page = a.page_size / kTileTokens;
-  const bool whole = tiles_per_page % TC == 0;
-  const int bytes = (whole ? TC : 1) * tile_bytes(D), per_page = whole ? tiles_per_page / TC : tiles_per_page;
-  const int per_step = whole ? 1 : TC;       // pieces of a step
-  const int pieces = lane < per_step ? (whole ? c0 + chunks : (hi_max + kTileTokens - 1) / kTileTokens) : 0;
-  const int ahead = per_step * step, ahead_pages = ahead / per_page, ahead_rest = ahead % per_page;
-  int piece = per_step * (c0 + w0) + lane, page_at = piece / per_page, in_page = piece % per_page;
-  int32_t page = w0 < chunks && piece < pieces ? table[page_at] : -1;
-  const uint8_t *head = a.cache + (int64_t)h * tiles_per_page * tile_bytes(D);
-  const int64_t page_bytes = (int64_t)a.Hkv * tiles_per_page * tile_bytes(D);
-  const uint64_t policy = policy_evict_first();
-  auto issue = [&](int c, int stage) {       // chunk c, and the look-up for chunk c + step
-    const bool want = piece < pieces, ok = want && page >= 0 && page < a.pages;
-    if (want && !ok) set_status(a.dev_status, DSPARK_ERR_PAGES);
-    const uint32_t got = __ballot_sync(0xffffffffu, ok);
-    if (lane == 0) mbar_arrive_tx(bar + 8 * stage, __popc(got) * bytes);
-    __syncwarp();
-    if (ok)
-      bulk_g2s(ring + stage * Sh::kStage + lane * tile_bytes(D), head + page * page_bytes + in_page * bytes, bytes,
-               bar + 8 * stage, policy);
-    piece += ahead;
-    page_at += ahead_pages;
-    in_page += ahead_rest;
-    if (in_page >= per_page) {
-      in_page -= per_page;
-      ++page_at;
+  int32_t page = -1;
+  {
+    const bool whole = tiles_per_page % TC == 0;
+    const int per_page = whole ? tiles_per_page / TC : tiles_per_page, per_step = whole ? 1 : TC;
+    const int ahead = per_step * step, pieces = whole ? c0 + chunks : (hi_max + kTileTokens - 1) / kTileTokens;
+    if (tid == 0) {
+      fixed[0] = make_int4(ahead, ahead / per_page, ahead % per_page, per_page);
+      fixed[1] = make_int4(whole ? TC * tile_bytes(D) : tile_bytes(D), pieces, h, chunks);
+      fixed[2] = make_int4((int)row0, total, first, 0);
     }
-    page = c + step < chunks && piece < pieces ? table[page_at] : -1;
+    if (lane < TC) {
+      const int piece = lane < per_step ? per_step * (c0 + w0) + lane : 0x3fffffff;
+      places[warp * TC + lane] = make_int4(piece, piece / per_page, piece % per_page, 0);
+      if (w0 < chunks && piece < pieces) page = table[piece / per_page];
+    }
+    __syncthreads();
+  }
+  auto issue = [&](int c, int stage) {       // chunk c, and the look-up for chunk c + step
+    if (lane < TC) {
+      constexpr uint32_t kLanes = (1u << TC) - 1;
+      const int4 by = fixed[0], k = fixed[1];
+      int4 at = places[warp * TC + lane];
+      const bool want = at.x < k.y, ok = want && page >= 0 && page < a.pages;
+      if (want && !ok) set_status(a.dev_status, DSPARK_ERR_PAGES);
+      const uint32_t got = __ballot_sync(kLanes, ok);
+      if (lane == 0) mbar_arrive_tx(bar + 8 * stage, __popc(got) * k.x);
+      __syncwarp(kLanes);
+      if (ok)
+        bulk_g2s(ring + stage * Sh::kStage + lane * tile_bytes(D),
+                 a.cache + ((int64_t)page * a.Hkv + k.z) * (tiles_per_page * tile_bytes(D)) + at.z * k.x, k.x,
+                 bar + 8 * stage, policy_evict_first());
+      at.x += by.x;
+      at.y += by.y;
+      at.z += by.z;
+      if (at.z >= by.w) {
+        at.z -= by.w;
+        ++at.y;
+      }
+      places[warp * TC + lane] = at;
+      page = c + step < k.w && at.x < k.y ? table[at.y] : -1;
+    }
   };
 #pragma unroll
   for (int i = 0; i < STAGES; ++i)
@@ -258,41 +322,30 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
 #pragma unroll
     for (int i = 0; i < KS / 2; ++i) lds<16>(q_smem + (i * 32 + lane) * 16, qf[i]);
   }
-  float rs[NT][2];                           // score of rows 2 q4 and 2 q4 + 1 = rs * accumulator, in log2; rs > 0
-  int hi[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int rr = 8 * nt + 2 * q4 + c, rho = first + rr;
-      rs[nt][c] = row_scale[rr];
-      hi[nt][c] = rho >= total ? 0 : (a.causal ? ctx + rho / a.group + 1 : (int)kv);
-    }
+  // score of rows 2 q4 and 2 q4 + 1 = row_scale * accumulator, in log2; row_scale > 0
+  const float2 *scales = reinterpret_cast<const float2 *>(row_scale) + q4;
+  auto end_of = [&](int nt, int k) {         // where the tokens end that such a row sees
+    const int rho = first + 8 * nt + 2 * q4 + k;
+    return rho >= total ? 0 : (a.causal ? ctx + rho / a.group + 1 : (int)kv);
+  };
 
-  // m: the running maximum in log2, moved when an accumulator passes bar_at; probabilities are 2^(score + z)
-  float o[NT][KS][4], m[NT][2], l[NT][2], z[NT][2], bar_at[NT][2];
+  // Probabilities are 2^(score + z), z = kLift - the running maximum in log2, which moves when an
+  // accumulator passes bar_at (-inf: no maximum yet, z = 0).
+  float o[NT][KS][4], l[NT][2], z[NT][2] = {}, bar_at[NT][2] = {};
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.0f;
-    m[nt][0] = m[nt][1] = bar_at[nt][0] = bar_at[nt][1] = -INFINITY;
+    bar_at[nt][0] = bar_at[nt][1] = -INFINITY;
     l[nt][0] = l[nt][1] = z[nt][0] = z[nt][1] = 0.0f;
   }
 
-  int stage = 0;
-  uint32_t phase = 0;
-  bool alive = true;
-  for (int c = w0; c < chunks; c += step) {
-    if (!mbar_try(bar + 8 * stage, phase) && !mbar_wait(bar + 8 * stage, phase, abort)) {
-      if (lane == 0) set_status(a.dev_status, DSPARK_ERR_DEVICE_TIMEOUT);
-      alive = false;
-      break;
-    }
-    const uint8_t *buf = smem + warp * Sh::kWarpBytes + stage * Sh::kStage;
-    const int base = (c0 + c) * kChunk;
-    const bool edge = base < lo_max || base + kChunk > hi_min;
+  auto maximum = [&](int nt, int k) { return bar_at[nt][k] == -INFINITY ? -INFINITY : kLift - z[nt][k]; };
+  // One chunk: buf holds its tiles, base is its first token; an EDGE one holds tokens that some row does not see.
+  auto step_on = [&](const uint8_t *buf, int base, auto kind) {
+    constexpr bool EDGE = decltype(kind)::value;
 
     float s[TC][NT][4];
 #pragma unroll
@@ -340,19 +393,21 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
     // masks and maxima
     bool rise = false;
     float top[NT][2];
-    if (edge) {
+    if constexpr (EDGE) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k) {
+          const int hi = end_of(nt, k);
 #pragma unroll
           for (int t = 0; t < TC; ++t)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               const int tok = base + 16 * t + 8 * b + g;
-              const bool seen = tok < hi[nt][k] && (!a.window || tok >= hi[nt][k] - a.window);
+              const bool seen = tok < hi && (!a.window || tok >= hi - a.window);
               if (!seen) s[t][nt][2 * b + k] = -INFINITY;
             }
+        }
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -366,17 +421,17 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        const float2 rs = scales[4 * nt];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float x = top[nt][k] * rs[nt][k];
+          float x = top[nt][k] * (k ? rs.y : rs.x);
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          const float up = fmaxf(m[nt][k], x);
-          const float f = m[nt][k] == -INFINITY ? 0.0f : fast_ex2(m[nt][k] - up);
-          m[nt][k] = up;
+          const float was = maximum(nt, k), up = fmaxf(was, x);
+          const float f = was == -INFINITY ? 0.0f : fast_ex2(was - up);
           z[nt][k] = up == -INFINITY ? 0.0f : kLift - up;
-          bar_at[nt][k] = (up + kLazy) / rs[nt][k];
+          bar_at[nt][k] = (up + kLazy) / (k ? rs.y : rs.x);
           l[nt][k] *= f;
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
@@ -391,22 +446,18 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
     uint32_t pb[TC][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const unsigned long long r2 = f2_pack(rs[nt][0], rs[nt][1]);
-      const unsigned long long z2 = f2_pack(z[nt][0], z[nt][1]);
-      unsigned long long l2 = f2_pack(l[nt][0], l[nt][1]);
+      const float2 rs = scales[4 * nt];
 #pragma unroll
       for (int t = 0; t < TC; ++t) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          float p0, p1;
-          f2_unpack(f2_fma(f2_pack(s[t][nt][2 * b], s[t][nt][2 * b + 1]), r2, z2), p0, p1);
-          p0 = fast_ex2(p0);
-          p1 = fast_ex2(p1);
-          l2 = f2_add(l2, f2_pack(p0, p1));
+          const float p0 = fast_ex2(fmaf(s[t][nt][2 * b], rs.x, z[nt][0]));
+          const float p1 = fast_ex2(fmaf(s[t][nt][2 * b + 1], rs.y, z[nt][1]));
+          l[nt][0] += p0;
+          l[nt][1] += p1;
           pb[t][nt][b] = transpose8x8(pack2(p0, p1));
         }
       }
-      f2_unpack(l2, l[nt][0], l[nt][1]);
     }
 
 #pragma unroll
@@ -418,7 +469,7 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
       const int group = g * (D / 8) / 16;
       uint32_t f0 = e4m3x2(lds_u16(tile + tile_vs(D, 2 * q4, group)));
       uint32_t f1 = e4m3x2(lds_u16(tile + tile_vs(D, 8 + 2 * q4, group)));
-      if (edge) {
+      if constexpr (EDGE) {
         // Tokens outside the tile's range hold nothing (a stale scale may be a NaN): they count 0.  A
         // scale that is a NaN inside it belongs to the rows that see its token alone, where 0 * NaN
         // would carry it to the others: it counts 0 too and then marks those rows' outputs.
@@ -440,7 +491,7 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                   for (int k = 0; k < 2; ++k)
-                    if (at < hi[nt][k] && (!a.window || at >= hi[nt][k] - a.window))
+                    if (const int hi = end_of(nt, k); at < hi && (!a.window || at >= hi - a.window))
 #pragma unroll
                       for (int i = 0; i < KS; ++i) o[nt][i][k] = o[nt][i][2 + k] = __int_as_float(0x7fffffff);
               }
@@ -464,6 +515,23 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
         }
       }
     }
+  };
+
+  int stage = 0;
+  uint32_t phase = 0;
+  bool alive = true;
+  for (int c = w0; c < chunks; c += step) {
+    if (!mbar_try(bar + 8 * stage, phase) && !mbar_wait(bar + 8 * stage, phase, abort)) {
+      if (lane == 0) set_status(a.dev_status, DSPARK_ERR_DEVICE_TIMEOUT);
+      alive = false;
+      break;
+    }
+    const uint8_t *buf = smem + warp * Sh::kWarpBytes + stage * Sh::kStage;
+    const int base = (c0 + c) * kChunk;
+    if (base < lo_max || base + kChunk > hi_min)
+      step_on(buf, base, std::true_type());
+    else
+      step_on(buf, base, std::false_type());
     __syncwarp();
     const int next = c + STAGES * step;
     if (next < chunks) issue(next, stage);
@@ -484,7 +552,9 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
     }
   }
 
-  if (a.partial) grid_dep_launch();
+  // what the loop had no registers for
+  const volatile int *kept = reinterpret_cast<const volatile int *>(fixed);
+  const int back[4] = {kept[8], kept[9], kept[10], kept[6]};
   // the CTA's warps meet
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -495,9 +565,9 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
       x += __shfl_xor_sync(0xffffffffu, x, 8);
       x += __shfl_xor_sync(0xffffffffu, x, 16);
       l[nt][k] = x;
-      if (x != x && m[nt][k] == -INFINITY) m[nt][k] = 0.0f;   // every score was a NaN: so is the result
+      if (x != x && bar_at[nt][k] == -INFINITY) bar_at[nt][k] = 0.0f, z[nt][k] = kLift;   // every score was a NaN
       if (g == 0) {
-        warp_m[warp * Sh::kRows + 8 * nt + 2 * q4 + k] = m[nt][k];
+        warp_m[warp * Sh::kRows + 8 * nt + 2 * q4 + k] = maximum(nt, k);
         warp_l[warp * Sh::kRows + 8 * nt + 2 * q4 + k] = x;
       }
     }
@@ -511,7 +581,7 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
       float big = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) big = fmaxf(big, warp_m[w * Sh::kRows + rr]);
-      const float f = m[nt][k] == -INFINITY ? 0.0f : fast_ex2(m[nt][k] - big);
+      const float mine_m = maximum(nt, k), f = mine_m == -INFINITY ? 0.0f : fast_ex2(mine_m - big);
       // a thread's dimensions of a row: chunk g, in order
 #pragma unroll
       for (int i = 0; i < KS; i += 2) {
@@ -549,7 +619,7 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
       part[tid] = cta_m[tid];
       part[Sh::kRows + tid] = cta_l[tid];
     }
-    if (chunks > rank * kWarps)
+    if (kept[7] > rank * kWarps)
       for (int i = tid; i < kVec; i += kWarps * 32)
         reinterpret_cast<float4 *>(part + 2 * Sh::kRows)[i] =
             *reinterpret_cast<const float4 *>(acc + i / (D / 4) * Sh::kOutRow + 4 * (i % (D / 4)));
@@ -562,8 +632,8 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
   else
     __syncthreads();
   for (int i = rank * kWarps * 32 + tid; i < kVec; i += cs * kWarps * 32) {
-    const int rr = i / (D / 4), d = 4 * (i % (D / 4)), rho = first + rr;
-    if (rho >= total) continue;
+    const int rr = i / (D / 4), d = 4 * (i % (D / 4)), rho = back[2] + rr;
+    if (rho >= back[1]) continue;
     float big = -INFINITY, sum = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int b = 0; b < cs; ++b) big = fmaxf(big, *cluster.map_shared_rank(cta_m + rr, b));
@@ -576,7 +646,7 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
       v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y), v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
     }
     const float inv = big == -INFINITY ? 0.0f : a.out_scale / sum;
-    const int64_t at = (row0 + rho / a.group) * a.Hq + h * a.group + rho % a.group;
+    const int64_t at = (int64_t)(back[0] + rho / a.group) * a.Hq + back[3] * a.group + rho % a.group;
     T y[4] = {Elem<DT>::from(v.x * inv), Elem<DT>::from(v.y * inv), Elem<DT>::from(v.z * inv),
               Elem<DT>::from(v.w * inv)};
     *reinterpret_cast<uint2 *>(reinterpret_cast<T *>(a.out) + at * D + d) = *reinterpret_cast<uint2 *>(y);
@@ -598,9 +668,10 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Atte
   const int rt = (int)(unit % row_tiles);
   unit /= row_tiles;
   const int h = (int)(unit % a.Hkv);
-  const int64_t r = unit / a.Hkv;
+  grid_dep_launch();
   grid_dep_wait();
-  if (r >= a.B || read_status(a.dev_status)) return;
+  if (unit / a.Hkv >= a.B || read_status(a.dev_status)) return;
+  const int64_t r = longest_first(a.kv_len, a.B, unit / a.Hkv, lane);
   const int64_t row0 = a.row_off[r], n = a.row_off[r + 1] - row0;
   const int64_t rho = (int64_t)rt * kRows + rr;
   if (rho >= n * a.group) return;
@@ -651,9 +722,9 @@ Plan plan_of(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows
   p.nt = rows <= 8 ? 1 : 2;
   p.row_tiles = (int)((rows + 8 * p.nt - 1) / (8 * p.nt));
   p.units = B * Hkv * p.row_tiles;
-  const int64_t slots = 2 * (int64_t)sms, least = kWarps * (int64_t)(4096 / D);   // tokens that give each warp a step
+  const int64_t slots = kCtas * (int64_t)sms, least = kWarps * (int64_t)(4096 / D);   // tokens that give each warp a step
   p.parts = 1;
-  while (p.parts < 8 && p.units * p.parts < 2 * slots && len >= 2 * p.parts * least) p.parts *= 2;
+  while (p.parts < 8 && p.units * p.parts < slots && len >= 2 * p.parts * least) p.parts *= 2;
   if (p.parts == 8 && p.units * 8 < slots) {
     const int64_t want = slots / p.units, most = len / least;
     const int64_t n = want < most ? want : most;
@@ -669,30 +740,14 @@ cudaError_t launch(const AttendArgs &a, const Plan &p, cudaStream_t s) {
   cudaError_t e = ensure_dynamic_smem((const void *)fn, Sh::kSmem);
   if (e != cudaSuccess) return e;
   if (p.units * p.parts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.units * p.parts));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = Sh::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = p.split ? 1 : p.parts;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fn, a, p.row_tiles, p.parts);
+  e = launch_next(fn, p.units * p.parts, kWarps * 32, Sh::kSmem, p.split ? 1 : p.parts, s, a, p.row_tiles, p.parts);
   if (e != cudaSuccess || !p.split) return e;
-  cfg.gridDim = dim3((unsigned)(p.units * NT * 2));
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<DT, D, NT>, a, p.row_tiles, p.parts);
+  return launch_next(merge_kernel<DT, D, NT>, p.units * NT * 2, 128, 0, 1, s, a, p.row_tiles, p.parts);
 }
 
 template <int DT, int D>
 cudaError_t launch_rows(const AttendArgs &a, const Plan &p, cudaStream_t s) {
-  return p.nt == 1 ? launch<DT, D, 1, 3, 2>(a, p, s) : launch<DT, D, 2, 2, 2>(a, p, s);
+  return p.nt == 1 ? launch<DT, D, 1, 2, kCtas>(a, p, s) : launch<DT, D, 2, 2, kCtas>(a, p, s);
 }
 
 }  // namespace
