@@ -14,6 +14,7 @@ import ctypes
 import math
 from typing import Optional
 
+import numpy as np
 import torch
 
 import speculative_decoding_draft_gb300 as _ds
@@ -127,7 +128,7 @@ class Rope:
         n = rotary_dim // 2
         own_gain = 1.0
         if inv_freq is None:
-            i = torch.arange(n, dtype=torch.float64)
+            i = np.arange(n, dtype=np.float64)
             if scaling == "ntk":
                 base = base * factor ** (rotary_dim / (rotary_dim - 2))
             inv = base ** (-2 * i / rotary_dim)
@@ -138,19 +139,19 @@ class Rope:
                     return rotary_dim * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
 
                 low, high = max(math.floor(pair_of(beta_fast)), 0), min(math.ceil(pair_of(beta_slow)), rotary_dim - 1)
-                ramp = ((i - low) / max(high - low, 0.001)).clamp(0, 1)
+                ramp = ((i - low) / max(high - low, 0.001)).clip(0, 1)
                 inv = inv * (1 - ramp) + inv / factor * ramp
                 own_gain = 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
         else:
-            inv = inv_freq.detach().to("cpu", torch.float64)
+            inv = inv_freq.detach().to("cpu", torch.float64).numpy()
             if inv.shape != (n,):
                 raise ValueError(f"inv_freq must have shape ({n},)")
-        self.inv_freq, self.rotary_dim, self.layout = inv, rotary_dim, layout
+        self.inv_freq, self.rotary_dim, self.layout = torch.from_numpy(inv), rotary_dim, layout
         self.gain = own_gain if gain is None else float(gain)
         # turns per position in 64-bit fixed point, wrapped: whole turns say nothing
         turn = inv / (2 * math.pi)
-        turn = turn - turn.round()                     # [-1/2, 1/2]: as a signed 64-bit fraction
-        self.turns = (turn * 2.0 ** 64).clamp(max=2.0 ** 63 - 1024).round().to(torch.int64).to(device)
+        turn = np.minimum((turn - np.rint(turn)) * 2.0 ** 64, 2.0 ** 63 - 1024)   # [-1/2, 1/2): a signed fraction
+        self.turns = torch.from_numpy(np.rint(turn).astype(np.int64)).to(device)
         self._c = _Rope(self.turns.data_ptr(), rotary_dim, layout == "interleaved", self.gain)
         self._at, self.device = ctypes.addressof(self._c), self.turns.get_device()
 
