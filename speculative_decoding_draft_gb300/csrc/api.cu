@@ -722,7 +722,7 @@ size_t dspark_attn_paged_workspace_bytes(int32_t q_heads, const dspark_cache *ca
   if (check_attend(q_heads, cache, where, max_rows) != DSPARK_OK || !device_info(&dev)) return 0;
   return (size_t)attend_workspace_bytes(where->B, cache->kv_heads, q_heads / cache->kv_heads, cache->head_dim,
                                         where->max_pages * cache->page_size,
-                                        max_rows < where->rows ? max_rows : where->rows, dev.sms);
+                                        max_rows < where->rows ? max_rows : where->rows, where->rows, dev.sms);
 }
 
 dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t dtype, const dspark_cache *cache,
@@ -752,7 +752,7 @@ dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t 
   a.out_scale = cache->v_scale;
   a.partial = (float *)workspace;
   a.dev_status = dev_status;
-  const int64_t need = attend_workspace_bytes(a.B, a.Hkv, a.group, a.D, a.max_pages * a.page_size, a.max_rows, dev.sms);
+  const int64_t need = attend_workspace_bytes(a.B, a.Hkv, a.group, a.D, a.max_pages * a.page_size, a.max_rows, a.rows, dev.sms);
   if (need && (!workspace || !aligned256(workspace) || workspace_bytes < (size_t)need)) return DSPARK_ERR_WORKSPACE;
   return launch_attend(a, (cudaStream_t)stream, dev.sms) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }

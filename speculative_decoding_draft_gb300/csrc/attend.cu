@@ -716,13 +716,16 @@ struct Plan {
   int64_t units;
 };
 
-Plan plan_of(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int sms) {
+Plan plan_of(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int64_t all_rows, int sms) {
   Plan p = {};
-  const int64_t rows = max_rows * group;
-  p.nt = rows <= 8 ? 1 : 2;
+  const int64_t rows = max_rows * group, mean_rows = all_rows / B;
+  // Tiles of 32 rows expand each stored element half as often as tiles of 16 but leave an SM 8 warps: better
+  // where they are mostly full (one request with 32 row-heads 77 us against 87), worse where requests have
+  // fewer rows than the largest (64 requests with 4 to 32: 90 us against 85).
+  p.nt = rows <= 8 ? 1 : (rows <= 16 || D != 128 || mean_rows * group <= 24 ? 2 : 4);
   p.row_tiles = (int)((rows + 8 * p.nt - 1) / (8 * p.nt));
   p.units = B * Hkv * p.row_tiles;
-  const int64_t slots = kCtas * (int64_t)sms, least = kWarps * (int64_t)(4096 / D);   // tokens that give each warp a step
+  const int64_t slots = (p.nt == 4 ? 2 : kCtas) * (int64_t)sms, least = kWarps * (int64_t)(4096 / D);   // tokens that give each warp a step
   p.parts = 1;
   while (p.parts < 8 && p.units * p.parts < slots && len >= 2 * p.parts * least) p.parts *= 2;
   if (p.parts == 8 && p.units * 8 < slots) {
@@ -747,18 +750,20 @@ cudaError_t launch(const AttendArgs &a, const Plan &p, cudaStream_t s) {
 
 template <int DT, int D>
 cudaError_t launch_rows(const AttendArgs &a, const Plan &p, cudaStream_t s) {
+  if constexpr (D == 128)
+    if (p.nt == 4) return launch<DT, D, 4, 2, 2>(a, p, s);
   return p.nt == 1 ? launch<DT, D, 1, 2, kCtas>(a, p, s) : launch<DT, D, 2, 2, kCtas>(a, p, s);
 }
 
 }  // namespace
 
-int64_t attend_workspace_bytes(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int sms) {
-  const Plan p = plan_of(B, Hkv, group, D, len, max_rows, sms);
+int64_t attend_workspace_bytes(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int64_t rows, int sms) {
+  const Plan p = plan_of(B, Hkv, group, D, len, max_rows, rows, sms);
   return p.split ? p.units * p.parts * 8 * p.nt * (D + 2) * 4 : 0;
 }
 
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s, int sms) {
-  const Plan p = plan_of(a.B, a.Hkv, a.group, a.D, a.max_pages * a.page_size, a.max_rows, sms);
+  const Plan p = plan_of(a.B, a.Hkv, a.group, a.D, a.max_pages * a.page_size, a.max_rows, a.rows, sms);
   AttendArgs b = a;
   if (!p.split) b.partial = nullptr;
   if (a.dtype == DSPARK_BF16)

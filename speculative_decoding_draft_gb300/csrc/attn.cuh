@@ -89,7 +89,7 @@ cudaError_t launch_cache_append(const HeadsArgs &a, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadArgs &a, cudaStream_t s);
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s, int sms);
 // Bytes of AttendArgs::partial that a call needs; len: tokens that its page table can name.
-int64_t attend_workspace_bytes(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int sms);
+int64_t attend_workspace_bytes(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int64_t rows, int sms);
 cudaError_t launch_penalize(const PenalizeArgs &a, cudaStream_t s, int sms);
 
 // A launch in clusters as a programmatic dependent of what precedes it in the stream, so that its CTAs
@@ -131,36 +131,43 @@ __device__ __forceinline__ int64_t request_of_row(const int32_t *row_off, int64_
   return lo;
 }
 
-// A row's place in the cache.  Returns false for rows past row_off[B] and for inconsistent
-// arguments, which are recorded in the status word.
+// A row's place in the cache, in two steps so that what needs the position alone need not wait for the
+// page: find_row looks the position up and starts the load of the page's id, place_row checks that.
+// Both return false for rows past row_off[B] and for inconsistent arguments, which they record in the
+// status word.  Loads that do not depend on one another are issued together.
 struct RowPlace {
   int64_t pos, tile;   // token position; index of its tile of head 0 in units of tiles
-  int t;               // token in the tile
+  int32_t page;
+  int in_page, t;      // its tile in the page, token in the tile
 };
-__device__ __forceinline__ bool place_row(const int32_t *row_off, const int32_t *kv_len, const int32_t *table, int64_t B,
-                                          int64_t max_pages, int64_t pages, int page_size, int Hkv, int64_t row,
-                                          int lane, int32_t *status, RowPlace *p) {
+__device__ __forceinline__ bool find_row(const int32_t *row_off, const int32_t *kv_len, const int32_t *table, int64_t B,
+                                         int64_t max_pages, int page_size, int64_t row, int lane, int32_t *status,
+                                         RowPlace *p) {
   const int64_t r = request_of_row(row_off, B, row, lane);
-  const int64_t a = row_off[r], b = row_off[r + 1];
+  const int64_t a = row_off[r], b = row_off[r + 1], all = row_off[B], len = kv_len[r];
   if (row < a || row >= b) {
-    if (row < row_off[B]) set_status(status, DSPARK_ERR_OFFSETS);
+    if (row < all) set_status(status, DSPARK_ERR_OFFSETS);
     return false;
   }
-  const int64_t pos = (int64_t)kv_len[r] - b + row;
+  const int64_t pos = len - b + row;
   if (pos < 0 || pos >= max_pages * page_size) {
     set_status(status, DSPARK_ERR_LENGTHS);
     return false;
   }
   // positions are below 2^31: a 32-bit division, the only one
   const uint32_t tile = (uint32_t)pos / kTileTokens, per = (uint32_t)page_size / kTileTokens, at = tile / per;
-  const int64_t page = table[r * max_pages + at];
-  if (page < 0 || page >= pages) {
+  p->page = table[r * max_pages + at];
+  p->pos = pos;
+  p->in_page = (int)(tile - at * per);
+  p->t = (int)((uint32_t)pos % kTileTokens);
+  return true;
+}
+__device__ __forceinline__ bool place_row(int64_t pages, int page_size, int Hkv, int32_t *status, RowPlace *p) {
+  if (p->page < 0 || p->page >= pages) {
     set_status(status, DSPARK_ERR_PAGES);
     return false;
   }
-  p->pos = pos;
-  p->tile = page * (Hkv * (int64_t)per) + (tile - at * per);
-  p->t = (int)((uint32_t)pos % kTileTokens);
+  p->tile = p->page * ((int64_t)Hkv * (page_size / kTileTokens)) + p->in_page;
   return true;
 }
 

@@ -210,13 +210,13 @@ __global__ void __launch_bounds__(kWarps * 32, APPEND ? 8 : 7)
   if (live && a.k_weight) w1 = load8<DT>(a.k_weight, 8 * sub);
   // A failed step, and a row that has no place, does nothing; but no copy may be under way at the end.
   RowPlace place = {};
-  const bool run = !read_status(a.dev_status) &&
-                   (!APPEND || place_row(a.row_off, a.kv_len, a.table, a.B, a.max_pages, a.pages, a.page_size, a.Hkv, row,
-                                         lane, a.dev_status, &place));
+  const int status = read_status(a.dev_status);          // looked at after the look-up, whose loads need not wait for it
+  const bool found = !APPEND || find_row(a.row_off, a.kv_len, a.table, a.B, a.max_pages, a.page_size, row, lane,
+                                         a.dev_status, &place);
   const int half = a.rot / 2;
   const bool turned = 8 * sub < a.rot;
   Pair c[4], s[4];
-  if (half && run) {
+  if (half && found) {
     const int64_t pos = (APPEND && !a.positions) ? place.pos : (int64_t)a.positions[row];
     float *C = CS[warp][0], *S = CS[warp][1];
     for (int i = lane; i < half; i += 32) {
@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kWarps * 32, APPEND ? 8 : 7)
     }
   };
 
+  const bool run = !status && found && (!APPEND || place_row(a.pages, a.page_size, a.Hkv, a.dev_status, &place));
   Pair w[4];
   to_pairs<DT>(part < n_q ? w0 : w1, w);
   const int beside = lane / LANES;
@@ -356,12 +357,12 @@ __device__ __forceinline__ uint32_t e2m1_to_e4m3(uint32_t c) {
 }
 
 __global__ void __launch_bounds__(kWarps * 32, 16) read_kernel(const __grid_constant__ CacheReadArgs a) {
-  if (read_status(a.dev_status)) return;
+  const int status = read_status(a.dev_status);
   const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   RowPlace p;
-  if (row >= a.rows || !place_row(a.row_off, a.kv_len, a.table, a.B, a.max_pages, a.pages, a.page_size, a.Hkv, row, lane,
-                                  a.dev_status, &p))
+  if (row >= a.rows || !find_row(a.row_off, a.kv_len, a.table, a.B, a.max_pages, a.page_size, row, lane, a.dev_status, &p) ||
+      !place_row(a.pages, a.page_size, a.Hkv, a.dev_status, &p) || status)
     return;
   // a lane's 4 bytes of codes are 8 elements; D/8 (a power of two) lanes take a head
   const int D = a.D, per = D / 8, w = D / 16, t = p.t, sub = lane & (per - 1), b = 4 * sub, beside = 32 / per;
