@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kWarps * 32, APPEND ? 8 : 7)
                                          a.dev_status, &place);
   const int half = a.rot / 2;
   const bool turned = 8 * sub < a.rot;
-  Pair c[4], s[4];
+  Pair c[4] = {}, s[4] = {};
   if (half && found) {
     const int64_t pos = (APPEND && !a.positions) ? place.pos : (int64_t)a.positions[row];
     float *C = CS[warp][0], *S = CS[warp][1];
@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kWarps * 32, APPEND ? 8 : 7)
   }
   const int other = !turned ? sub : (8 * sub < half ? sub + a.rot / 16 : sub - a.rot / 16);
   const float inv_d = 1.0f / (float)D;
+  const bool whole = a.rot == 8 * LANES;     // every lane's dimensions turn
   // norm (with a weight) and rotation of the heads that the warp holds
   auto turn_heads = [&](Pair (&x)[4], bool normed, const Pair (&w)[4]) {
     if (normed) {
@@ -268,9 +269,10 @@ __global__ void __launch_bounds__(kWarps * 32, APPEND ? 8 : 7)
           y[e] = pair_of(__shfl_sync(0xffffffffu, f.x, other, LANES), __shfl_sync(0xffffffffu, f.y, other, LANES));
         }
       }
-      if (turned) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = f2_fma(x[e], c[e], f2_mul(y[e], s[e]));
+      for (int e = 0; e < 4; ++e) {          // a select, not a branch that lanes take apart
+        const Pair z = f2_fma(x[e], c[e], f2_mul(y[e], s[e]));
+        x[e] = whole || turned ? z : x[e];
       }
     }
   };
