@@ -749,6 +749,7 @@ dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t 
   a.causal = causal != 0, a.window = (int)window, a.max_rows = (int)(max_rows < where->rows ? max_rows : where->rows);
   a.dtype = dtype;
   a.scale_log2 = scale * cache->k_scale * kLog2e;
+  if (!std::isfinite(a.scale_log2)) return DSPARK_ERR_DIMS;
   a.out_scale = cache->v_scale;
   a.partial = (float *)workspace;
   a.dev_status = dev_status;
@@ -765,7 +766,7 @@ dspark_status dspark_logits_penalize(const void *logits, int32_t dtype, int64_t 
     return DSPARK_ERR_NULL;
   if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return DSPARK_ERR_DTYPE;
   if (rows < 1 || rows > kMaxRows || V < 2 || V > kMaxV || B < 1 || B > kMaxB || p->hist_cap < 1 ||
-      (V + 1023) / 1024 * B > kMaxRows || p->hist_cap > kMaxRows || p->bias_cap < 0 || p->bias_cap > 4096 || (p->draft_tok && p->draft_cap < 1))
+      (V + 1023) / 1024 * B > kMaxRows || p->hist_cap > (1 << 30) || p->bias_cap < 0 || p->bias_cap > 4096 || (p->draft_tok && p->draft_cap < 1))
     return DSPARK_ERR_DIMS;
   DeviceInfo dev;
   if (!device_info(&dev)) return DSPARK_ERR_CUDA;

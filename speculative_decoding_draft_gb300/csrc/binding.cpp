@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -209,6 +210,7 @@ PyObject *norm_rope(PyObject *const *v) {
   const void *wq = maybe(v[4], "q_weight", dt, {d}, dev), *wk = maybe(v[5], "k_weight", dt, {d}, dev);
   st.status(v[8], dev);
   if (rows) {
+    const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
     const int e = api.norm_rope(&qh, v[1] == Py_None ? nullptr : &kh, rows, (int32_t)hq, (int32_t)hkv, (int32_t)d, code, pos,
                                 rope, wq, wk, (float)real(v[6]), qo.data, ko.data, (int32_t *)st.data, stream_of(v[9], dev));
     if (e) return PyLong_FromLong(e);
@@ -241,6 +243,7 @@ PyObject *append(PyObject *const *v) {
   const void *wk = maybe(v[9], "k_weight", dt, {d}, dev), *wq = maybe(v[11], "q_weight", dt, {d}, dev);
   st.status(v[14], dev);
   if (rows) {
+    const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
     const int e = api.append(&kh, &vh, qo.data ? &qh : nullptr, (int32_t)hq, code, cache, &where, pos, rope, wq, wk,
                              (float)real(v[12]), qo.data, (int32_t *)st.data, stream_of(v[15], dev));
     if (e) return PyLong_FromLong(e);
@@ -263,6 +266,7 @@ PyObject *read(PyObject *const *v) {
   vs.make(v[6], "v_scale", at::kFloat8_e4m3fn, {rows, h, d / 16}, dev);
   st.status(v[7], dev);
   if (rows) {
+    const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
     const int e = api.read(cache, &where, k.data, ks.data, vo.data, vs.data, (int32_t *)st.data, stream_of(v[8], dev));
     if (e) return PyLong_FromLong(e);
   }
@@ -289,6 +293,7 @@ PyObject *paged(PyObject *const *v) {
   if (PyObject_IsTrue(v[10])) lse.make(v[11], "lse", at::kFloat, {rows, hq}, dev);
   st.status(v[13], dev);
   if (rows) {
+    const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
     const int64_t need = (int64_t)api.workspace_bytes((int32_t)hq, cache, &where, max_rows);
     int64_t have = 0;
     if (need) {
@@ -350,6 +355,7 @@ PyObject *penalize(PyObject *const *v) {
   o.make(v[12], "logits", z.scalar_type(), {rows, V}, dev);
   st.status(v[13], dev);
   if (rows) {
+    const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
     const int e = api.penalize(in, code, rows, V, B, off, &p, o.data, (int32_t *)st.data, stream_of(v[14], dev));
     if (e) return PyLong_FromLong(e);
   }

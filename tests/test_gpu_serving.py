@@ -370,6 +370,67 @@ def test_attend_over_a_cache_past_four_gigabytes():
     attend_check(q, got, held, [2, 1], kv, d ** -0.5, True, 0)
 
 
+@pytest.mark.parametrize("n,kv,d,hkv,group,page", [
+    ([300], [333], 128, 2, 4, 64),                     # a prompt chunk: many tiles of 32 rows
+    ([70, 1, 130], [70, 500, 140], 64, 1, 3, 32),
+    ([1] * 300, [3 * i % 97 for i in range(300)], 64, 1, 2, 16),      # more requests than are put in order
+    ([8], [20000], 128, 1, 4, 64),                     # one key/value head: split through the workspace
+    ([2], [40000], 64, 2, 1, 48)])
+def test_attend_shapes_of_the_launch(n, kv, d, hkv, group, page):
+    g = gen(len(n) + d)
+    table, pages = paged(g, kv, page)
+    cache, held = filled(g, kv, table, pages, hkv, d, page)
+    q = randn(g, sum(n), hkv * group, d).half()
+    got = ds.attend_paged(q, cache, offsets(n), i32(kv), table, max_rows=max(n), want_lse=True)
+    ok(got["status"])
+    attend_check(q, got, held, n, kv, d ** -0.5, True, 0)
+    again = ds.attend_paged(q, cache, offsets(n), i32(kv), table, max_rows=max(n), want_lse=True,
+                            workspace=got["workspace"])
+    assert torch.equal(again["out"], got["out"]) and torch.equal(again["lse"], got["lse"])       # the order of sums is fixed
+
+
+def test_heads_with_gaps_between_them():
+    g, d, n, kv = gen(21), 64, [5, 2], [25, 40]
+    table, pages = paged(g, kv, 16)
+    x = randn(g, 7, 9, d + 24).bfloat16()[..., :d]      # a head's rows do not follow one another
+    q, k, v = x[:, :5], x[:, 5:7], x[:, 7:]
+    pos, rope, w = i32(list(range(7))), ds.Rope(d), (1 + 0.1 * randn(g, d)).bfloat16()
+    a, b = (ds.norm_rope(*t, pos, rope, q_weight=w) for t in ((q, k), (q.contiguous(), k.contiguous())))
+    assert torch.equal(a["q"], b["q"]) and torch.equal(a["k"], b["k"])
+    kept = []
+    for t in ((q, k, v), (q.contiguous(), k.contiguous(), v.contiguous())):
+        cache = ds.PagedCache.empty(pages, 2, d, 16)
+        got = ds.cache_append(cache, t[1], t[2], offsets(n), i32(kv), table, rope=rope, k_weight=w, q=t[0], q_weight=w)
+        out = ds.attend_paged(t[0][:, :4], cache, offsets(n), i32(kv), table)
+        kept.append((got["q"], cache.data, out["out"]))
+    assert all(torch.equal(s, t) for s, t in zip(*kept))
+
+
+def test_attend_workspace():
+    import ctypes
+    from speculative_decoding_draft_gb300 import serving as sv
+    g, d, kv = gen(22), 128, [9000]
+    table, pages = paged(g, kv, 64)
+    cache, _ = filled(g, kv, table, pages, 1, d, 64)
+    q, off, lens = randn(g, 1, 2, d).bfloat16(), offsets([1]), i32(kv)
+    st, out = ds.new_status("cuda"), torch.empty(1, 2, d, device="cuda").bfloat16()
+    where = sv._Ragged(off.data_ptr(), lens.data_ptr(), table.data_ptr(), 1, 1, table.shape[1])
+    heads, L = sv._Heads(q.data_ptr(), 2 * d, d), ds.lib()
+    need = L.dspark_attn_paged_workspace_bytes(2, cache._c, where, 1)
+    assert need > 0
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+
+    def call(at, size):
+        return L.dspark_attn_paged(heads, 2, 1, cache._c, where, 1, 0.1, 1, 0, out.data_ptr(), None, at, size,
+                                   st.data_ptr(), None)
+    assert call(None, 0) == 10 and call(ws.data_ptr(), need - 1) == 10 and call(ws.data_ptr() + 16, need) == 10
+    assert call(ws.data_ptr(), need) == 0
+    ok(st)
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")          # too small a one is replaced
+    got = ds.attend_paged(q, cache, off, lens, table, scale=0.1, workspace=small)
+    assert torch.equal(got["out"], out) and got["workspace"].numel() >= need
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # penalties
 # ---------------------------------------------------------------------------------------------------------------
