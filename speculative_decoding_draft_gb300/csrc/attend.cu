@@ -51,7 +51,10 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
-constexpr int kCtas = 4;              // on an SM together
+constexpr int kStages = 2;            // of a warp's ring; three took 2 us more, shared memory that CTAs want
+// CTAs on an SM together by the n-tiles of a warp: what their registers allow without spilling in the loop
+// (16 rows at 4 CTAs spill 35 words a step: 85 us for the 64 requests against 76 at 3)
+__host__ __device__ constexpr int ctas_of(int nt) { return nt == 1 ? 4 : (nt == 2 ? 3 : 2); }
 constexpr float kLazy = 8.0f;         // how far (log2) a score may pass the running maximum
 constexpr float kLift = 6.0f;         // probabilities are kept 2^kLift up
 
@@ -150,36 +153,36 @@ __device__ __forceinline__ int64_t longest_first(const int32_t *kv_len, int64_t 
   return i;                                  // not reached
 }
 
-template <int D, int NT, int STAGES>
+template <int D, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
   static constexpr int kTiles = 256 / D;                           // tiles of a warp's step: 64 or 32 tokens
   static constexpr int kChunk = kTiles * kTileTokens;
   static constexpr int kStage = kTiles * tile_bytes(D);
-  static constexpr int kRing = STAGES * kStage;                    // per warp
+  static constexpr int kRing = kStages * kStage;                    // per warp
   static constexpr int kOutRow = D + 4;                            // floats; padded against bank conflicts
   static constexpr int kOut = kRows * kOutRow * 4;                 // one warp's partial output
   static constexpr int kWarpBytes = (kRing > kOut ? kRing : kOut); // the ring is reused for it
   static constexpr bool kQShared = NT > 1;                         // query fragments stay in shared memory
   static constexpr int kQ = NT * (D / 16) * 32 * 8;
-  static constexpr int kBars = kWarps * STAGES * 8;
+  static constexpr int kBars = kWarps * kStages * 8;
   static constexpr int kMl = kWarps * kRows * 8 + kRows * 12;      // maxima and sums of the warps, of the CTA; scales
   static constexpr int kPlaces = kWarps * kTiles * 16 + 48;        // the ring's places, see below
   static constexpr int kSmem = kWarps * kWarpBytes + kQ + kBars + kPlaces + kMl + 16;
   static constexpr int kPartial = kRows * (D + 2);                 // floats of a CTA's partial result
 };
 
-template <int DT, int D, int NT, int STAGES, int MINB>
-__global__ void __launch_bounds__(kWarps * 32, MINB)
+template <int DT, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : ctas_of(NT))
     attend_kernel(const __grid_constant__ AttendArgs a, int row_tiles, int parts) {
   using T = typename Elem<DT>::T;
-  using Sh = Shape<D, NT, STAGES>;
+  using Sh = Shape<D, NT>;
   constexpr int KS = D / 16;                 // k-steps of q.k, and m-tiles of the output
   constexpr int TC = Sh::kTiles, kChunk = Sh::kChunk;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *q_smem = smem + kWarps * Sh::kWarpBytes;
   uint64_t *bars = reinterpret_cast<uint64_t *>(q_smem + Sh::kQ);
-  int4 *places = reinterpret_cast<int4 *>(bars + kWarps * STAGES), *fixed = places + kWarps * TC;
+  int4 *places = reinterpret_cast<int4 *>(bars + kWarps * kStages), *fixed = places + kWarps * TC;
   float *warp_m = reinterpret_cast<float *>(fixed + 3);
   float *warp_l = warp_m + kWarps * Sh::kRows;
   float *cta_m = warp_l + kWarps * Sh::kRows, *cta_l = cta_m + Sh::kRows;
@@ -222,9 +225,9 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
   const int chunks = skip || hi_max <= 0 ? 0 : (hi_max + kChunk - 1) / kChunk - c0;
 
   const uint32_t ring = smem_u32(smem) + warp * Sh::kWarpBytes;
-  const uint32_t bar = smem_u32(bars + warp * STAGES);
+  const uint32_t bar = smem_u32(bars + warp * kStages);
   if (lane == 0) {
-    for (int i = 0; i < STAGES; ++i) mbar_init(bar + 8 * i, 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(bar + 8 * i, 1);
     if (warp == 0) *abort = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
     }
   };
 #pragma unroll
-  for (int i = 0; i < STAGES; ++i)
+  for (int i = 0; i < kStages; ++i)
     if (w0 + i * step < chunks) issue(w0 + i * step, i);
 
   // Queries, an n-tile a warp: a lane has row g, dimensions [q4 D/4, (q4 + 1) D/4).
@@ -533,19 +536,19 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
     else
       step_on(buf, base, std::false_type());
     __syncwarp();
-    const int next = c + STAGES * step;
+    const int next = c + kStages * step;
     if (next < chunks) issue(next, stage);
-    if (++stage == STAGES) {
+    if (++stage == kStages) {
       stage = 0;
       phase ^= 1;
     }
   }
   if (!alive) {   // a wait gave up: the copies still on their way get one more bounded wait each
-    for (int i = 0; i < STAGES; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       const long long t0 = clock64();
       while (!mbar_try(bar + 8 * stage, phase) && clock64() - t0 < kTimeoutCycles / 8) {
       }
-      if (++stage == STAGES) {
+      if (++stage == kStages) {
         stage = 0;
         phase ^= 1;
       }
@@ -725,7 +728,7 @@ Plan plan_of(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows
   p.nt = rows <= 8 ? 1 : (rows <= 16 || D != 128 || mean_rows * group <= 24 ? 2 : 4);
   p.row_tiles = (int)((rows + 8 * p.nt - 1) / (8 * p.nt));
   p.units = B * Hkv * p.row_tiles;
-  const int64_t slots = (p.nt == 4 ? 2 : kCtas) * (int64_t)sms, least = kWarps * (int64_t)(4096 / D);   // tokens that give each warp a step
+  const int64_t slots = ctas_of(p.nt) * (int64_t)sms, least = kWarps * (int64_t)(4096 / D);   // tokens that give each warp a step
   p.parts = 1;
   while (p.parts < 8 && p.units * p.parts < slots && len >= 2 * p.parts * least) p.parts *= 2;
   if (p.parts == 8 && p.units * 8 < slots) {
@@ -736,10 +739,10 @@ Plan plan_of(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows
   return p;
 }
 
-template <int DT, int D, int NT, int STAGES, int MINB>
+template <int DT, int D, int NT>
 cudaError_t launch(const AttendArgs &a, const Plan &p, cudaStream_t s) {
-  using Sh = Shape<D, NT, STAGES>;
-  auto *fn = attend_kernel<DT, D, NT, STAGES, MINB>;
+  using Sh = Shape<D, NT>;
+  auto *fn = attend_kernel<DT, D, NT>;
   cudaError_t e = ensure_dynamic_smem((const void *)fn, Sh::kSmem);
   if (e != cudaSuccess) return e;
   if (p.units * p.parts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -751,8 +754,8 @@ cudaError_t launch(const AttendArgs &a, const Plan &p, cudaStream_t s) {
 template <int DT, int D>
 cudaError_t launch_rows(const AttendArgs &a, const Plan &p, cudaStream_t s) {
   if constexpr (D == 128)
-    if (p.nt == 4) return launch<DT, D, 4, 2, 2>(a, p, s);
-  return p.nt == 1 ? launch<DT, D, 1, 2, kCtas>(a, p, s) : launch<DT, D, 2, 2, kCtas>(a, p, s);
+    if (p.nt == 4) return launch<DT, D, 4>(a, p, s);
+  return p.nt == 1 ? launch<DT, D, 1>(a, p, s) : launch<DT, D, 2>(a, p, s);
 }
 
 }  // namespace
