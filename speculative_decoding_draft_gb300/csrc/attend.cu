@@ -29,16 +29,17 @@
 // start longest first.
 //
 // Measured (one GB300): 64 requests of 512 to 4096 tokens with 1 to 8 rows, 32 query and 8 key/value heads
-// of 128 dimensions 85 us (26 us of reading at the memory's rate); one request of 131071 tokens with 8 rows
-// 87 us (22); 256 requests of up to 16384 tokens, heads of 64 dimensions, 266 us (202).  Bound by the issue
-// slots: a warp's step of 32 tokens by 16 rows is 760 instructions, 136 of them conversions and 128 scalings,
-// both at half rate, and 64 products; the SMs issue 2 a cycle.  Tried and slower or no faster: 32 rows a warp
-// (8 warps an SM: 158 us for the 64 requests), 8 rows (104), two warps sharing a step of 32 rows with half of
-// the output each (133; one request: 85), chunks drawn from a counter instead of dealt (also not
-// reproducible), 24 warps an SM.  The fifth-generation tensor cores take operands from shared or tensor
-// memory only, where every expanded element would have to be written and read again: 1 KB a token and head
-// each way against the 144 bytes that are stored, 3 times what shared memory can move in the time that the
-// stored bytes take to arrive.
+// of 128 dimensions 76 us (26 us of reading at the memory's rate); one request of 131071 tokens with 8 rows
+// 77 us (22); 256 requests of up to 16384 tokens, heads of 64 dimensions, 265 us (202).  Bound by the issue
+// slots and what fills them: a warp's step of 32 tokens by 16 rows is about 700 instructions, 136 of them
+// conversions and 128 scalings, both at half rate, and 64 products; the SMs issue 1.8 to 2.2 a cycle.
+// Tried and slower or no faster for the 64 requests: 16 warps an SM with 35 words spilled a step (85 us), 32
+// rows a warp (90), 8 rows (104), two warps sharing a step of 32 rows with half of the output each (133), steps
+// of 16 tokens (84) and of 64 (86), chunks drawn from a counter instead of dealt (no faster, and not
+// reproducible).  The fifth-generation tensor cores take operands from shared or tensor memory only, where
+// every expanded element would have to be written and read again: 1 KB a token and head each way against the
+// 144 bytes that are stored, 3 times what shared memory can move in the time that the stored bytes take to
+// arrive.
 #include <type_traits>
 
 #include <cooperative_groups.h>
@@ -126,7 +127,7 @@ __device__ __forceinline__ uint32_t lds_u16(const uint8_t *p) { return *reinterp
 __device__ __forceinline__ uint32_t lds_u8(const uint8_t *p) { return *p; }
 
 // The i-th request, long ones first: CTAs start in the order of their index, and one that starts last must
-// not be the longest.  Eight classes by length; every warp works it out by itself from the lengths, as
+// not be the longest (64 requests 85 us, 97 in the order given; 256 requests 266, 300).  Eight classes by length; every warp works it out by itself from the lengths, as
 // long as it can hold these (B <= 256; with more requests the last CTAs weigh little).
 constexpr int kOrderMost = 256;
 __device__ __forceinline__ int64_t longest_first(const int32_t *kv_len, int64_t B, int64_t i, int lane) {
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : ctas_of(NT))
   if (first >= total) return;
   const int last = (first + Sh::kRows < total ? first + Sh::kRows : total) - 1;
   // a step that failed does no work, but its CTAs still meet their cluster below
-  const bool skip = read_status(a.dev_status) != 0;
+  const bool skip = status_on_entry(a.dev_status) != 0;
 
   // what the tile's rows see: from [lo_min, lo_max] up to [hi_min, hi_max]
   const int ctx = (int)(kv - n);
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Atte
   const int h = (int)(unit % a.Hkv);
   grid_dep_launch();
   grid_dep_wait();
-  if (unit / a.Hkv >= a.B || read_status(a.dev_status)) return;
+  if (unit / a.Hkv >= a.B || status_on_entry(a.dev_status)) return;
   const int64_t r = longest_first(a.kv_len, a.B, unit / a.Hkv, lane);
   const int64_t row0 = a.row_off[r], n = a.row_off[r + 1] - row0;
   const int64_t rho = (int64_t)rt * kRows + rr;
@@ -724,7 +725,7 @@ Plan plan_of(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows
   const int64_t rows = max_rows * group, mean_rows = all_rows / B;
   // Tiles of 32 rows expand each stored element half as often as tiles of 16 but leave an SM 8 warps: better
   // where they are mostly full (one request with 32 row-heads 77 us against 87), worse where requests have
-  // fewer rows than the largest (64 requests with 4 to 32: 90 us against 85).
+  // fewer rows than the largest (64 requests with 4 to 32: 90 us against 76).
   p.nt = rows <= 8 ? 1 : (rows <= 16 || D != 128 || mean_rows * group <= 24 ? 2 : 4);
   p.row_tiles = (int)((rows + 8 * p.nt - 1) / (8 * p.nt));
   p.units = B * Hkv * p.row_tiles;

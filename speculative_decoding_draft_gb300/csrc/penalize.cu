@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads, DT == DSPARK_F32 ? 4 : 5) penalize_k
   const int slices = (int)((a.V + slice - 1) / slice);
   const int r = (int)(blockIdx.x / (unsigned)slices), V = (int)a.V;      // V <= 2^30, B <= 2^20
   const int v0 = (int)(blockIdx.x - (unsigned)(r * slices)) * slice, width = min(V - v0, slice);
-  const int status = read_status(a.dev_status);
+  const int status = status_on_entry(a.dev_status);
   const int64_t first = a.row_off[r], end = a.row_off[r + 1];
   const int64_t n_hist = a.hist_len[r], n_prompt = a.prompt_len[r];
   const float rep = a.repetition[r], pre = a.presence[r], fre = a.frequency[r];

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kWarps * 32, APPEND ? 8 : 7)
   if (live && a.k_weight) w1 = load8<DT>(a.k_weight, 8 * sub);
   // A failed step, and a row that has no place, does nothing; but no copy may be under way at the end.
   RowPlace place = {};
-  const int status = read_status(a.dev_status);          // looked at after the look-up, whose loads need not wait for it
+  const int status = status_on_entry(a.dev_status);          // looked at after the look-up, whose loads need not wait for it
   const bool found = !APPEND || find_row(a.row_off, a.kv_len, a.table, a.B, a.max_pages, a.page_size, row, lane,
                                          a.dev_status, &place);
   const int half = a.rot / 2;
@@ -359,7 +359,7 @@ __device__ __forceinline__ uint32_t e2m1_to_e4m3(uint32_t c) {
 }
 
 __global__ void __launch_bounds__(kWarps * 32, 16) read_kernel(const __grid_constant__ CacheReadArgs a) {
-  const int status = read_status(a.dev_status);
+  const int status = status_on_entry(a.dev_status);
   const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   RowPlace p;
