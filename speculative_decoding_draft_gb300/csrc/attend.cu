@@ -54,8 +54,8 @@ namespace cg = cooperative_groups;
 constexpr int kWarps = 4;
 constexpr int kStages = 2;            // of a warp's ring; three took 2 us more, shared memory that CTAs want
 // CTAs on an SM together by the n-tiles of a warp: what their registers allow without spilling in the loop
-// (16 rows at 4 CTAs spill 35 words a step: 85 us for the 64 requests against 76 at 3)
-__host__ __device__ constexpr int ctas_of(int nt) { return nt == 1 ? 4 : (nt == 2 ? 3 : 2); }
+// (16 rows at 4 CTAs spill 35 words a step: 85 us for the 64 requests against 76 at 3).
+__host__ __device__ constexpr int ctas_of(int nt, int D) { return nt == 4 ? 2 : (nt == 1 && D == 64 ? 4 : 3); }
 constexpr float kLazy = 8.0f;         // how far (log2) a score may pass the running maximum
 constexpr float kLift = 6.0f;         // probabilities are kept 2^kLift up
 
@@ -174,7 +174,7 @@ struct Shape {
 };
 
 template <int DT, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : ctas_of(NT))
+__global__ void __launch_bounds__(kWarps * 32, ctas_of(NT, D))
     attend_kernel(const __grid_constant__ AttendArgs a, int row_tiles, int parts) {
   using T = typename Elem<DT>::T;
   using Sh = Shape<D, NT>;
@@ -729,14 +729,16 @@ Plan plan_of(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows
   p.nt = rows <= 8 ? 1 : (rows <= 16 || D != 128 || mean_rows * group <= 24 ? 2 : 4);
   p.row_tiles = (int)((rows + 8 * p.nt - 1) / (8 * p.nt));
   p.units = B * Hkv * p.row_tiles;
-  const int64_t slots = ctas_of(p.nt) * (int64_t)sms, least = kWarps * (int64_t)(4096 / D);   // tokens that give each warp a step
+  const int64_t slots = ctas_of(p.nt, D) * (int64_t)sms, least = kWarps * (int64_t)(4096 / D);   // tokens that give each warp a step
   p.parts = 1;
   while (p.parts < 8 && p.units * p.parts < slots && len >= 2 * p.parts * least) p.parts *= 2;
-  if (p.parts == 8 && p.units * 8 < slots) {
-    const int64_t want = slots / p.units, most = len / least;
-    const int64_t n = want < most ? want : most;
-    if (n > 8) p.parts = (int)(n < 1024 ? n : 1024), p.split = true;
-  }
+  // Few units with much to read: one wave of CTAs exactly, joined by a kernel of its own, where clusters of
+  // eight leave most SMs idle (one row over 131071 tokens 44 us, 116 in clusters) or, with one or two
+  // requests and so CTAs of one length, start a second wave (40 rows over 30000 tokens 83 us against 132).
+  // Otherwise clusters are as fast or faster: 8 requests of up to 20000 tokens 35 us against 41.  A warp has
+  // 8 steps at least, or the joining costs more than it gains (8000 tokens: 22 us against 12.6).
+  const int64_t wave = slots / p.units, deep = len / (8 * least), n = wave < deep ? wave : deep;
+  if (p.parts >= 4 && n > 1 && (n > p.parts || (B <= 2 && p.units * p.parts > slots))) p.parts = (int)(n < 1024 ? n : 1024), p.split = true;
   return p;
 }
 

@@ -374,7 +374,7 @@ def test_attend_over_a_cache_past_four_gigabytes():
     ([300], [333], 128, 2, 4, 64),                     # a prompt chunk: many tiles of 32 rows
     ([70, 1, 130], [70, 500, 140], 64, 1, 3, 32),
     ([1] * 300, [3 * i % 97 for i in range(300)], 64, 1, 2, 16),      # more requests than are put in order
-    ([8], [20000], 128, 1, 4, 64),                     # one key/value head: split through the workspace
+    ([8], [40000], 128, 1, 4, 64),                     # one key/value head: split through the workspace
     ([2], [40000], 64, 2, 1, 48)])
 def test_attend_shapes_of_the_launch(n, kv, d, hkv, group, page):
     g = gen(len(n) + d)
@@ -409,7 +409,7 @@ def test_heads_with_gaps_between_them():
 def test_attend_workspace():
     import ctypes
     from speculative_decoding_draft_gb300 import serving as sv
-    g, d, kv = gen(22), 128, [9000]
+    g, d, kv = gen(22), 128, [40000]              # long enough to be split
     table, pages = paged(g, kv, 64)
     cache, _ = filled(g, kv, table, pages, 1, d, 64)
     q, off, lens = randn(g, 1, 2, d).bfloat16(), offsets([1]), i32(kv)
