@@ -25,9 +25,10 @@ constexpr int kRowsAhead = 2;                 // rows whose loads are in flight 
 constexpr int64_t kMaxRequestRows = (1 << 20) - 1;
 constexpr uint32_t kInPrompt = 0x80000000u;   // a count's top bit
 
-struct Bias {
+struct Bias {      // an entry of the request's list that falls into the slice
   int32_t at;
-  float sum;
+  float value;
+  int32_t index;   // in the list
 };
 
 template <int DT, bool MASK>
@@ -37,8 +38,8 @@ __global__ void __launch_bounds__(kThreads, DT == DSPARK_F32 ? 4 : 5) penalize_k
   constexpr uint32_t kAll = (1u << N) - 1;
   extern __shared__ uint32_t counts[];        // [slice]
   uint32_t *map = counts + slice;             // [slice / 32]: listed tokens
-  Bias *biases = reinterpret_cast<Bias *>(map + slice / 32);                                     // [bias slots]
-  uint16_t *list = reinterpret_cast<uint16_t *>(biases + (a.bias_cap < slice ? a.bias_cap : slice));   // [slice]
+  Bias *biases = reinterpret_cast<Bias *>(map + slice / 32);                        // [bias_cap], in no order
+  uint16_t *list = reinterpret_cast<uint16_t *>(biases + a.bias_cap);               // [slice]
   __shared__ int n_list, n_bias;
   const int tid = threadIdx.x;
   const int slices = (int)((a.V + slice - 1) / slice);
@@ -99,17 +100,11 @@ __global__ void __launch_bounds__(kThreads, DT == DSPARK_F32 ? 4 : 5) penalize_k
       else if (tok >= v0 && tok < v0 + width)
         mark((int)(tok - v0));
     }
-  for (int64_t k = tid; k < a.bias_cap; k += kThreads) {
-    const int32_t *tok = a.bias_tok + (int64_t)r * a.bias_cap;
-    if (tok[k] < v0 || tok[k] >= v0 + width) continue;   // -1 pads the list
-    bool again = false;
-    for (int64_t b = 0; b < k; ++b) again |= tok[b] == tok[k];
-    if (again) continue;
-    float sum = 0.0f;                                    // a token listed twice: its biases add up in their order
-    for (int64_t b = k; b < a.bias_cap; ++b)
-      if (tok[b] == tok[k]) sum += a.bias_val[(int64_t)r * a.bias_cap + b];
-    biases[atomicAdd(&n_bias, 1)] = Bias{(int32_t)(tok[k] - v0), sum};
-    mark((int)(tok[k] - v0));
+  for (int k = tid; k < (int)a.bias_cap; k += kThreads) {
+    const uint32_t at = (uint32_t)(a.bias_tok[(int64_t)r * a.bias_cap + k] - v0);
+    if (at >= (uint32_t)width) continue;                 // another slice's, or the padding's -1
+    biases[atomicAdd(&n_bias, 1)] = Bias{(int32_t)at, a.bias_val[(int64_t)r * a.bias_cap + k], k};
+    mark((int)at);
   }
 
   // First pass.  Pieces lie on 16-byte boundaries of memory; what a row's slice has before its first
@@ -208,8 +203,15 @@ __global__ void __launch_bounds__(kThreads, DT == DSPARK_F32 ? 4 : 5) penalize_k
       for (int k = 0; k < j; ++k) times += draft[k] == (int32_t)(v0 + at);
     if (times || prompted) z = z > 0.0f ? __fdiv_rn(z, rep) : z * rep;
     if (times) z = z - pre - fre * (float)times;
-    for (int b = 0; b < n_bias; ++b)
-      if (biases[b].at == at) z += biases[b].sum;
+    float sum = 0.0f;                                    // a token listed twice: its biases add up in the list's order
+    for (int done = -1, next = 0; n_bias > 0 && next < INT32_MAX; done = next) {
+      float value = 0.0f;
+      next = INT32_MAX;
+      for (int b = 0; b < n_bias; ++b)
+        if (biases[b].at == at && biases[b].index > done && biases[b].index < next) next = biases[b].index, value = biases[b].value;
+      sum += value;
+    }
+    z += sum;
     *p = Elem<DT>::from(z);
   }
 }
@@ -219,8 +221,7 @@ cudaError_t launch(const PenalizeArgs &a, cudaStream_t s, int sms) {
   // Larger slices read the history less often, smaller ones give a few requests more CTAs.
   int slice = kSlice;
   while (slice > 1024 && a.B * ((a.V + slice - 1) / slice) < 4 * sms) slice /= 2;
-  const int64_t bias_slots = a.bias_cap < slice ? a.bias_cap : slice;
-  const int smem = slice * 4 + slice / 8 + (int)bias_slots * 8 + slice * 2;
+  const int smem = slice * 4 + slice / 8 + (int)a.bias_cap * (int)sizeof(Bias) + slice * 2;
   cudaError_t e = ensure_dynamic_smem((const void *)penalize_kernel<DT, MASK>, smem);
   if (e != cudaSuccess) return e;
   penalize_kernel<DT, MASK><<<(unsigned)(a.B * ((a.V + slice - 1) / slice)), kThreads, smem, s>>>(a, slice);

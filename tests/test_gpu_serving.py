@@ -437,7 +437,7 @@ def test_attend_workspace():
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("n,V,cap,n_bias,mask,draft", [
     ([1], 2, 1, 0, False, False), ([3, 0, 1], 33, 5, 2, True, True), ([4, 2], 4095, 300, 5, True, True),
-    ([2, 8], 4097, 64, 0, True, True), ([1, 1, 5], 10000, 1000, 40, False, True), ([8], 131072, 5000, 3, True, False)])
+    ([2, 8], 4097, 64, 0, True, True), ([1, 1, 5], 10000, 1000, 40, False, True), ([8], 131072, 5000, 3, True, False), ([2, 1], 3000, 7, 4096, False, True)])
 def test_penalize(dtype, n, V, cap, n_bias, mask, draft):
     g, dt, B, rows, K = gen(V + cap), DTYPES[dtype], len(n), sum(n), max(n)
     ints = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device="cuda", dtype=torch.int32)  # noqa: E731
