@@ -104,7 +104,7 @@ __device__ __forceinline__ int status_on_entry(const int32_t *status) {
 // A launch in clusters as a programmatic dependent of what precedes it in the stream, so that its CTAs
 // stand ready when that ends: such a kernel waits (grid_dep_wait) before its first access to global
 // memory and lets the next one in (grid_dep_launch) at once.  For the attention, which needs this form
-// of launch for its clusters and its joining kernel: a single token's call takes 8.8 us (10.2 without).
+// of launch for its clusters and its joining kernel: a single token's call takes 7.9 us (10.2 without).
 // The other operators' plain launches cost the host 1 us less, which is what bounds their small calls.
 template <class... P>
 cudaError_t launch_next(void (*kernel)(P...), int64_t grid, int threads, int smem, int cluster, cudaStream_t s, P... args) {
