@@ -613,3 +613,61 @@ def test_bindings_refuse():
             pytest.fail(f"case {i} was taken")
     empty = ds.attend_paged(q[:0], cache, i32([0, 0]), lens, table)
     assert empty["out"].shape == (0, 4, d)
+
+
+def guarded(shape, dtype):
+    """A tensor inside a larger one whose surroundings hold a pattern, and a check of these."""
+    n, pad, size = math.prod(shape), 4096, torch.empty(0, dtype=dtype).element_size()
+    whole = torch.full((n * size + 2 * pad,), 0xA5, dtype=torch.uint8, device="cuda")
+    inside = whole[pad: pad + n * size].view(dtype).view(shape)
+    return inside, lambda: bool((whole[:pad] == 0xA5).all() and (whole[pad + n * size:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("d,hq,hkv,n,kv,page,V", [(128, 12, 4, [3, 1], [90, 33], 16, 1003), (64, 5, 5, [7], [7], 32, 33)])
+def test_nothing_is_written_around_the_outputs(d, hq, hkv, n, kv, page, V):
+    g, rows, B = gen(31), sum(n), len(n)
+    table, pages = paged(g, kv, page)
+    off, lens = offsets(n), i32(kv)
+    x = randn(g, rows, hq + 2 * hkv, d).bfloat16()
+    q, k, v = x[:, :hq], x[:, hq: hq + hkv], x[:, hq + hkv:]
+    f8, bf = torch.float8_e4m3fn, torch.bfloat16
+    checks = []
+
+    def room(shape, dtype):
+        t, check = guarded(shape, dtype)
+        checks.append(check)
+        return t
+
+    rope = ds.Rope(d)
+    ds.norm_rope(q, k, off.new_zeros(rows), rope, out=dict(q=room((rows, hq, d), bf), k=room((rows, hkv, d), bf)))
+    data = room((pages, hkv, page // 16, 18 * d), torch.uint8)
+    data.zero_()
+    cache = ds.PagedCache(data, page)
+    ds.cache_append(cache, k, v, off, lens, table, rope=rope, q=q, out=dict(q=room((rows, hq, d), bf)))
+    ds.cache_read(cache, off, lens, table, rows, out=dict(
+        k=room((rows, hkv, d), f8), v=room((rows, hkv, d), f8), k_scale=room((rows, hkv, d // 16), f8),
+        v_scale=room((rows, hkv, d // 16), f8)))
+    ds.attend_paged(q, cache, off, lens, table, max_rows=max(n), want_lse=True,
+                    out=dict(out=room((rows, hq, d), bf), lse=room((rows, hq), torch.float32)))
+    one = torch.ones(B, device="cuda")
+    for dtype in (bf, torch.float32):
+        z = randn(g, rows, V).to(dtype)
+        mask = torch.randint(-2 ** 31, 2 ** 31 - 1, (rows, (V + 31) // 32), generator=g, device="cuda", dtype=torch.int32)
+        ds.penalize_logits(z, off, i32([[V - 1, 0]] * B), i32([2] * B), i32([1] * B), one, one, one,
+                           draft_tok=i32([[V - 1] * max(n)] * B), mask=mask, out=dict(logits=room((rows, V), dtype)))
+    torch.cuda.synchronize()
+    assert all(c() for c in checks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_penalize_where_input_and_output_lie_differently(dtype):
+    g, dt, n, V = gen(32), DTYPES[dtype], [2, 1], 517
+    flat = randn(g, 3 * V + 1).to(dt)
+    z = flat[1:].view(3, V)                                 # one element off a 16-byte boundary
+    mask = torch.randint(-2 ** 31, 2 ** 31 - 1, (3, (V + 31) // 32), generator=g, device="cuda", dtype=torch.int32)
+    one = torch.full((2,), 1.5, device="cuda")
+    args = (offsets(n), i32([[5, 9, 5], [516, 0, 1]]), i32([3, 2]), i32([1, 0]), one, one, one)
+    for m in (None, mask):
+        want = ds.penalize_logits(z.clone(), *args, mask=m)["logits"]
+        assert torch.equal(ds.penalize_logits(z, *args, mask=m)["logits"], want)
+    assert torch.equal(ds.penalize_logits(z, *args, mask=mask, out=dict(logits=z))["logits"], want)
