@@ -127,8 +127,9 @@ __device__ __forceinline__ uint32_t lds_u16(const uint8_t *p) { return *reinterp
 __device__ __forceinline__ uint32_t lds_u8(const uint8_t *p) { return *p; }
 
 // The i-th request, long ones first: CTAs start in the order of their index, and one that starts last must
-// not be the longest (64 requests 85 us, 97 in the order given; 256 requests 266, 300).  Eight classes by length; every warp works it out by itself from the lengths, as
-// long as it can hold these (B <= 256; with more requests the last CTAs weigh little).
+// not be the longest (64 requests 85 us, 97 in the order given; 256 requests 266, 300).  Eight classes by
+// length; every warp works it out by itself from the lengths, as long as it can hold these (B <= 256; with
+// more requests the last CTAs weigh little).
 constexpr int kOrderMost = 256;
 __device__ __forceinline__ int64_t longest_first(const int32_t *kv_len, int64_t B, int64_t i, int lane) {
   if (B > kOrderMost || B < 2) return i;
