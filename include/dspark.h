@@ -490,8 +490,8 @@ typedef struct {
   int64_t B, rows, max_pages;
 } dspark_ragged;
 
-/* y = x rsqrt(mean(x^2) + eps) weight per head (where a weight [head_dim] of the call's dtype is
- * given), then the rotation (rope NULL: none), in fp32, rounded once.  q_out [rows, q_heads, D] and
+/* y = x rsqrt(mean(x^2) + eps) weight per head (where a weight [head_dim] of the call's dtype,
+ * 16-byte aligned, is given), then the rotation (rope NULL: none), in fp32, rounded once.  q_out [rows, q_heads, D] and
  * k_out [rows, kv_heads, D] are contiguous and may be the inputs themselves when those are; k and k_out may be NULL.
  * positions [rows] int32.  head_dim: a multiple of 16 to 256.  F32, BF16, F16. */
 dspark_status dspark_attn_norm_rope(const dspark_heads *q, const dspark_heads *k, int64_t rows, int32_t q_heads,

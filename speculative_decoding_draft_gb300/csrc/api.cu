@@ -587,6 +587,11 @@ dspark_status check_heads(const dspark_heads &t, int dtype) {
   return DSPARK_OK;
 }
 
+// Norm weights are read 16 bytes at a time.
+dspark_status check_weights(const void *q_weight, const void *k_weight) {
+  return aligned16(q_weight) && aligned16(k_weight) ? DSPARK_OK : DSPARK_ERR_UNSUPPORTED;
+}
+
 dspark_status check_rope(const dspark_rope *rope, int head_dim) {
   if (!rope) return DSPARK_OK;
   if (!rope->turns) return DSPARK_ERR_NULL;
@@ -632,6 +637,7 @@ dspark_status dspark_attn_norm_rope(const dspark_heads *q, const dspark_heads *k
     return DSPARK_ERR_DIMS;
   dspark_status st = check_heads(*q, dtype);
   if (st == DSPARK_OK && k) st = check_heads(*k, dtype);
+  if (st == DSPARK_OK) st = check_weights(q_weight, k_weight);
   if (st == DSPARK_OK) st = check_rope(rope, head_dim);
   if (st != DSPARK_OK) return st;
   if (!aligned16(q_out) || !aligned16(k_out)) return DSPARK_ERR_UNSUPPORTED;
@@ -662,6 +668,7 @@ dspark_status dspark_attn_append(const dspark_heads *k, const dspark_heads *v, c
   if (st == DSPARK_OK) st = check_heads(*k, dtype);
   if (st == DSPARK_OK) st = check_heads(*v, dtype);
   if (st == DSPARK_OK && q) st = check_heads(*q, dtype);
+  if (st == DSPARK_OK) st = check_weights(q_weight, k_weight);
   if (st == DSPARK_OK) st = check_rope(rope, cache->head_dim);
   if (st != DSPARK_OK) return st;
   if ((q && (q_heads < 1 || q_heads > kMaxHeads)) || !(eps >= 0.0f)) return DSPARK_ERR_DIMS;

@@ -72,6 +72,13 @@ T *maybe(PyObject *o, const char *name, at::ScalarType dtype, at::IntArrayRef sh
   return o == Py_None ? nullptr : like<T>(o, name, dtype, shape, dev);
 }
 
+// A norm weight [dim] or None, which the kernels read 16 bytes at a time.
+const void *weight(PyObject *o, const char *name, at::ScalarType dtype, int64_t dim, int dev) {
+  const void *p = maybe(o, name, dtype, {dim}, dev);
+  if ((uintptr_t)p % 16) refuse(PyExc_ValueError, std::string(name) + " must start on a 16-byte boundary");
+  return p;
+}
+
 // A [rows, heads, dim] tensor whose last dimension is dense; rows and heads may be strided.
 dspark_heads heads(PyObject *o, const char *name, at::ScalarType dtype, int64_t rows, int64_t n, int64_t dim, int dev) {
   const at::Tensor &t = cuda_tensor(o, name);
@@ -207,7 +214,7 @@ PyObject *norm_rope(PyObject *const *v) {
   const dspark_rope *rope = rope_for(v[3], d);
   const int32_t *pos = nullptr;
   if (rope || v[2] != Py_None) pos = like<int32_t>(v[2], "positions", at::kInt, {rows}, dev);
-  const void *wq = maybe(v[4], "q_weight", dt, {d}, dev), *wk = maybe(v[5], "k_weight", dt, {d}, dev);
+  const void *wq = weight(v[4], "q_weight", dt, d, dev), *wk = weight(v[5], "k_weight", dt, d, dev);
   st.status(v[8], dev);
   if (rows) {
     const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
@@ -240,7 +247,7 @@ PyObject *append(PyObject *const *v) {
   }
   const dspark_rope *rope = rope_for(v[8], d);
   const int32_t *pos = maybe<int32_t>(v[7], "positions", at::kInt, {rows}, dev);
-  const void *wk = maybe(v[9], "k_weight", dt, {d}, dev), *wq = maybe(v[11], "q_weight", dt, {d}, dev);
+  const void *wk = weight(v[9], "k_weight", dt, d, dev), *wq = weight(v[11], "q_weight", dt, d, dev);
   st.status(v[14], dev);
   if (rows) {
     const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);

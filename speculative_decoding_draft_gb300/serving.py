@@ -162,7 +162,7 @@ def norm_rope(q, k=None, positions=None, rope: Optional[Rope] = None, *, q_weigh
 
     q [rows, Hq, D], k [rows, Hkv, D] or None (float32, bfloat16 or float16; D a multiple of 16 to 256; rows and
     heads may be strided, as in a view of a fused projection), positions [rows] int32 (with a rope), q_weight /
-    k_weight [D] or None (no norm).  Returns q and k of the inputs' shape, contiguous (``out`` may name the
+    k_weight [D], on a 16-byte boundary, or None (no norm).  Returns q and k of the inputs' shape, contiguous (``out`` may name the
     inputs themselves where those are contiguous).
     """
     turn = None if rope is None else _of(rope, Rope, "rope")._at

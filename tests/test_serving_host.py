@@ -54,6 +54,17 @@ def test_norm_rope_refusals(lib):
     assert call(q=heads(264)) == call(q=heads(row=1028)) == call(k=heads(head=4)) == call(out=264) == "UNSUPPORTED"
 
 
+def test_norm_weights_off_a_boundary_are_refused(lib):
+    # refused where the heads are, before the rope and eps of these calls are looked at
+    rope = sv._Rope(ONE, 80, 0, 1.0)
+    for wq, wk, want in ((ONE, ONE, "DIMS"), (ONE + 8, None, "UNSUPPORTED"), (None, ONE + 2, "UNSUPPORTED"),
+                         (ONE, ONE + 4, "UNSUPPORTED")):
+        assert name(lib.dspark_attn_norm_rope(heads(), heads(), 2, 4, 2, 64, 1, ONE, rope, wq, wk, 1e-6, ONE, ONE, ONE,
+                                              None)) == want
+        assert name(lib.dspark_attn_append(heads(), heads(), heads(), 4, 1, cache(), ragged(), None, None, wq, wk, -1.0,
+                                           ONE, ONE, None)) == want
+
+
 def test_cache_refusals(lib):
     def append(k=heads(), v=heads(), q=None, hq=0, dtype=1, c=None, w=None, rope=None, eps=0.0, q_out=None, st=ONE):
         return name(lib.dspark_attn_append(k, v, q, hq, dtype, c or cache(), w or ragged(), None, rope, None, None, eps,
