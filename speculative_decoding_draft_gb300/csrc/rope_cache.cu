@@ -91,6 +91,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // a NaN stays
   return c;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float c;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+  return c;
+}
+
 // Sine and cosine of an angle of turn / 2^32 turns: the nearest quarter turn by integers, the rest
 // (up to pi / 4) by the Taylor series, whose first terms left out are below 2^-29 and 2^-25.
 __device__ __forceinline__ void sin_cos(uint32_t turn, float *sn, float *cs) {
@@ -121,14 +127,13 @@ __device__ __forceinline__ uint32_t quantize8(const Pair (&x)[4], float inv, uin
     top = max_nan(top, max_nan(fabsf(f.x), fabsf(f.y)));
   }
   top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  float sixth = top * inv;
-  if (EXACT) {
-    sixth = __fdiv_rn(sixth, 6.0f);
-  } else {
-    // Six times the border of two scales has 7 bits, so a 16-bit value's sixth is a border exactly or off
-    // it by 2^-12: rounded to 21 bits the product, off by 2^-23, meets the borders without a division.
-    sixth = __uint_as_float((__float_as_uint(sixth * (1.0f / 6.0f)) + 4u) & ~7u);
-  }
+  // The sixth, correctly rounded: the product with 1/6 and one step of the remainder, which fp32 holds exactly.
+  // Six times the border of two scales has 7 bits, so a sixth that is no border lies at least half a step of
+  // fp32 off it and does not round to it.  A NaN stays one; what the largest scale is too small for (infinities
+  // among it) is cut where the remainder is still finite.
+  const float most = min_nan(top * inv, 1048576.0f);
+  const float about = most * (1.0f / 6.0f);
+  const float sixth = fmaf(fmaf(about, -6.0f, most), 1.0f / 6.0f, about);
   const __nv_fp8_storage_t s8 = __nv_cvt_float_to_fp8(sixth, __NV_SATFINITE, __NV_E4M3);
   *scale = s8;
   // 0 (nothing to keep) and NaN (nothing else to say) leave the elements 0
