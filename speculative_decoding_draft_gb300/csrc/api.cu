@@ -688,7 +688,7 @@ dspark_status dspark_attn_append(const dspark_heads *k, const dspark_heads *v, c
   a.rows = where->rows, a.Hq = q ? q_heads : 0, a.Hkv = cache->kv_heads, a.D = cache->head_dim, a.dtype = dtype;
   a.eps = eps;
   a.cache = (uint8_t *)cache->data, a.pages = cache->pages, a.page_size = cache->page_size;
-  a.k_inv = 1.0f / cache->k_scale, a.v_inv = 1.0f / cache->v_scale;
+  a.k_unit = cache->k_scale, a.v_unit = cache->v_scale, a.k_inv = 1.0f / a.k_unit, a.v_inv = 1.0f / a.v_unit;
   a.B = where->B, a.max_pages = where->max_pages;
   a.row_off = where->row_off, a.kv_len = where->kv_len, a.table = where->page_table;
   a.dev_status = dev_status;

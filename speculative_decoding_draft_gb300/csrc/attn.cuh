@@ -45,7 +45,7 @@ struct HeadsArgs {
   uint8_t *cache;
   int64_t pages, max_pages, B;
   int page_size;
-  float k_inv, v_inv;
+  float k_inv, v_inv, k_unit, v_unit;   // the cache's scales and their reciprocals, powers of two
   const int32_t *row_off, *kv_len, *table;
   int32_t *dev_status;
 };

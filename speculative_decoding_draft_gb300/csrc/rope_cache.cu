@@ -116,10 +116,14 @@ __device__ __forceinline__ void sin_cos(uint32_t turn, float *sn, float *cs) {
   *cs = (quarter + 1) & 2 ? -b : b;
 }
 
-// One lane's 8 elements of a group of 16 as codes, and the group's scale.  The lane beside holds the
-// others; inv is a power of two.
-template <bool EXACT>
-__device__ __forceinline__ uint32_t quantize8(const Pair (&x)[4], float inv, uint8_t *scale) {
+// One lane's 8 elements of a group of 16 as codes, and the group's scale.  The lane beside holds the others;
+// unit is a power of two, inv = 1 / unit.
+//
+// Both quotients, by 6 and by the scale, are correctly rounded: the product with the reciprocal and one step of
+// the remainder, which fp32 holds exactly as the divisor has 4 bits at most.  A quotient that is no border of
+// two codes (or scales) lies at least half a step of fp32 off it and does not round to it, so what is stored
+// is the nearest to y, for normed and turned keys with all the bits of fp32 as for 16-bit values.
+__device__ __forceinline__ uint32_t quantize8(const Pair (&x)[4], float inv, float unit, uint8_t *scale) {
   float top = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -127,10 +131,8 @@ __device__ __forceinline__ uint32_t quantize8(const Pair (&x)[4], float inv, uin
     top = max_nan(top, max_nan(fabsf(f.x), fabsf(f.y)));
   }
   top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  // The sixth, correctly rounded: the product with 1/6 and one step of the remainder, which fp32 holds exactly.
-  // Six times the border of two scales has 7 bits, so a sixth that is no border lies at least half a step of
-  // fp32 off it and does not round to it.  A NaN stays one; what the largest scale is too small for (infinities
-  // among it) is cut where the remainder is still finite.
+  // a NaN stays one; what the largest scale is too small for (infinities among it) is cut to where the
+  // remainder is finite
   const float most = min_nan(top * inv, 1048576.0f);
   const float about = most * (1.0f / 6.0f);
   const float sixth = fmaf(fmaf(about, -6.0f, most), 1.0f / 6.0f, about);
@@ -139,23 +141,22 @@ __device__ __forceinline__ uint32_t quantize8(const Pair (&x)[4], float inv, uin
   // 0 (nothing to keep) and NaN (nothing else to say) leave the elements 0
   if ((s8 & 0x7f) == 0 || (s8 & 0x7f) == 0x7f) return 0;
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)));
+  float back;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(back) : "f"(s));
+  const float down = -s * unit;
+  back *= inv;
+  const Pair b2 = pair_of(back, back), d2 = pair_of(down, down);
   Pair z[4];
-  if (EXACT) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = floats_of(x[i]);
-      z[i] = pair_of(__fdiv_rn(f.x * inv, s), __fdiv_rn(f.y * inv, s));
+  for (int i = 0; i < 4; ++i) {
+    z[i] = f2_mul(x[i], b2);
+    const Pair fine = f2_fma(f2_fma(z[i], d2, x[i]), b2, z[i]);
+    if (s8 == 0x7e) {                        // elements past the largest have no remainder to speak of, or a NaN
+      const float2 q = floats_of(z[i]), f = floats_of(fine);
+      z[i] = pair_of(fabsf(q.x) < 8.0f ? f.x : q.x, fabsf(q.y) < 8.0f ? f.y : q.y);
+    } else {
+      z[i] = fine;
     }
-  } else {
-    // The quotient of a value of up to 11 bits by a scale of 4 is the border of two codes exactly or
-    // off it by 2^-13 at least.  The product with the reciprocal is off by 2^-19.7 at most (up to 6.4):
-    // rounded to a multiple of 2^-18 it meets the borders exactly, without a division.
-    float back;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(back) : "f"(s));
-    back *= inv;
-    const Pair b2 = pair_of(back, back), up = pair_of(48.0f, 48.0f), down = pair_of(-48.0f, -48.0f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] = f2_add(f2_add(f2_mul(x[i], b2), up), down);
   }
   uint32_t codes = 0;
 #pragma unroll
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kWarps * 32, APPEND ? 8 : 7)
 #pragma unroll
     for (int i = 0; i < 2; ++i, to += kBeside * tile_step) {
       uint8_t scale;
-      const uint32_t codes = quantize8<DT == DSPARK_F32>(x[i], is_v ? a.v_inv : a.k_inv, &scale);
+      const uint32_t codes = quantize8(x[i], is_v ? a.v_inv : a.k_inv, is_v ? a.v_unit : a.k_unit, &scale);
       if (live && left > i * kBeside) {
         *reinterpret_cast<uint32_t *>(to + (is_v ? v_at : k_at)) = codes;
         if (!(sub & 1)) to[is_v ? vs_at : ks_at] = scale;

@@ -1,5 +1,5 @@
 """The operators around a ragged verification step where they once went wrong: norm weights off their boundary, NaN in
-16-bit keys and values."""
+16-bit keys and values, elements and scales at the borders of their codes."""
 import math
 
 import pytest
@@ -59,6 +59,82 @@ def test_attention_sees_the_nan_of_a_key_or_value_of_any_type(dtype, part):
     assert torch.isnan(got["out"][2:, :, 16:32]).all()
     assert torch.isnan(got["lse"][2:]).all() == (part == "k")
     attend_check(q[:2], got, [tuple(t[:37] for t in held[0])], [2], [37], d ** -0.5, True, 0)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_append_of_infinities_and_of_values_past_the_largest_scale(dtype):
+    d, dt = 64, DTYPES[dtype]
+    big = 6e4 if dt == torch.float16 else 1e30
+    x = torch.ones(1, 1, d, device="cuda").to(dt)
+    x[0, 0, 3], x[0, 0, 17], x[0, 0, 18], x[0, 0, 34], x[0, 0, 50] = math.inf, -math.inf, math.inf, -big, 2688
+    x[0, 0, 51] = -2240                                    # 5 times the largest scale: a tie, to the even code
+    cache = ds.PagedCache.empty(1, 1, d, 16)
+    where = (i32([0, 1]), i32([1]), i32([[0]]))
+    ok(ds.cache_append(cache, x, x, *where)["status"])
+    got = ds.cache_read(cache, *where, 1)
+    want = torch.zeros(d, device="cuda")
+    want[3], want[17], want[18], want[34], want[50], want[51] = 6, -6, 6, -6, 6, -4
+    for h in ("k", "v"):
+        assert (got[h + "_scale"].float() == 448).all() and torch.equal(got[h].float().flatten(), want)
+
+
+EDGES = (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)
+
+
+def nearest(y):
+    """Elements and scales of y (64 bits), a tie to the even code.  A quotient that is no border lies further from it
+    than 64 bits round."""
+    y = y.unflatten(-1, (-1, 16))
+    s = (y.abs().amax(-1) / 6).clamp(max=448).to(torch.float8_e4m3fn).double()
+    z = torch.where(s[..., None] > 0, y / s[..., None], 0.0)
+    code = torch.zeros_like(z, dtype=torch.long)
+    for i, e in enumerate(EDGES):
+        code += (z.abs() > e) if i % 2 == 0 else (z.abs() >= e)
+    return (torch.tensor(E2M1, dtype=torch.float64, device=y.device)[code] * z.sign()).flatten(-2), s
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("unit", [1.0, 2.0 ** -5, 2.0 ** 9])
+def test_append_takes_the_nearest_code_at_every_border(dtype, unit):
+    # a group for each scale: its largest element gives that scale, the others lie at a border of two codes and one
+    # step of the type to either side of it
+    dt, d = DTYPES[dtype], 64
+    scales = torch.arange(1, 127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).float()
+    edges = torch.tensor(EDGES, device="cuda")
+    at = (scales[:, None] * edges * unit).to(dt)
+    assert torch.equal(at.double(), scales.double()[:, None] * edges.double() * unit) or dt == torch.float16
+    rows = []
+    for step in (-1, 0, 1):
+        x = torch.zeros(126, 16, device="cuda").to(dt)
+        x[:, 0] = (scales * 6 * unit).to(dt)
+        x[:, 1:8] = (at.view(torch.int32 if dt == torch.float32 else torch.int16) + step).view(dt)
+        x[:, 8:15] = -x[:, 1:8]
+        rows.append(x)
+    x = torch.cat(rows + [torch.zeros(2, 16, device="cuda").to(dt)]).view(-1, 1, d)
+    x = torch.where(x.isfinite(), x, 0)
+    n = x.shape[0]
+    where = (i32([0, n]), i32([n]), i32([list(range(-(-n // 16)))]))
+    cache = ds.PagedCache.empty(-(-n // 16), 1, d, 16, k_scale=unit, v_scale=unit)
+    ok(ds.cache_append(cache, x, x, *where)["status"])
+    got = ds.cache_read(cache, *where, n)
+    want, s = nearest(x.double() / unit)
+    for h in ("k", "v"):
+        assert torch.equal(got[h + "_scale"].double(), s) and torch.equal(got[h].double(), want)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("layout,d", [("half", 128), ("interleaved", 64)])
+def test_append_takes_the_nearest_codes_of_normed_and_turned_keys(dtype, layout, d):
+    # a normed and turned key has all the bits of fp32, as norm_rope gives them of the same heads in fp32
+    g, dt, n, hkv = gen(43), DTYPES[dtype], 8192, 8
+    k, w, rope = randn(g, n, hkv, d).to(dt), (1 + 0.1 * randn(g, d)).to(dt), ds.Rope(d, layout=layout)
+    where = (i32([0, n]), i32([n]), i32([list(range(n // 64))]))
+    cache = ds.PagedCache.empty(n // 64, hkv, d, 64, k_scale=0.5)
+    ok(ds.cache_append(cache, k, k, *where, rope=rope, k_weight=w)["status"])
+    got = ds.cache_read(cache, *where, n)
+    y = ds.norm_rope(k.float(), None, i32(list(range(n))), rope, q_weight=w.float())["q"]
+    e, s = nearest(y.double() / 0.5)
+    assert torch.equal(got["k_scale"].double(), s) and torch.equal(got["k"].double(), e)
 
 
 def test_norm_weights_off_a_boundary_are_refused():
