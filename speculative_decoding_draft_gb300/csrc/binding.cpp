@@ -17,6 +17,7 @@
 
 #include <cmath>
 #include <initializer_list>
+#include <optional>
 #include <string>
 
 #include "dspark.h"
@@ -105,14 +106,49 @@ dspark_ragged ragged(PyObject *row_off, PyObject *kv_len, PyObject *table, int64
           like<int32_t>(table, "page_table", at::kInt, {B, width}, dev), B, rows, width};
 }
 
-// out[key], checked, or a new tensor; `holder` gets the Python object.
+void *address(PyObject *o) {
+  void *p = o == Py_None ? nullptr : PyLong_AsVoidPtr(o);
+  if (!p && PyErr_Occurred()) throw Refused();
+  return p;
+}
+
+// The stream of a call.  A given one is the current one for as long as this lives: what the call allocates, the fill
+// of its status word and its kernels follow one another on it, and memory that the caller drops at once is not used
+// again before they are done.  What it returns counts as used by the caller's current stream too.
+class Stream {
+ public:
+  Stream(PyObject *given, int dev) : dev_((c10::DeviceIndex)dev) {
+    if (given == Py_None) return;
+    const cudaStream_t s = (cudaStream_t)address(given);
+    before_ = c10::cuda::getCurrentCUDAStream(dev_);
+    here_.reset_stream(s && s != cudaStreamLegacy ? c10::cuda::getStreamFromExternal(s, dev_)
+                                                  : c10::cuda::getDefaultCUDAStream(dev_));
+  }
+  int device() const { return dev_; }
+  void *raw() const { return (void *)c10::cuda::getCurrentCUDAStream(dev_).stream(); }
+  // A Python object of a tensor that the call has made.
+  PyObject *hand_out(at::Tensor t) const {
+    if (before_ && before_->stream() != raw()) t.record_stream(before_->unwrap());
+    PyObject *o = THPVariable_Wrap(std::move(t));
+    if (!o) throw Refused();
+    return o;
+  }
+
+ private:
+  c10::DeviceIndex dev_;
+  std::optional<c10::cuda::CUDAStream> before_;
+  c10::cuda::OptionalCUDAStreamGuard here_;
+};
+
+// out[key], checked, or a new tensor.
 struct Result {
   PyObject *object = nullptr;
   void *data = nullptr;
   Result() = default;
   Result(const Result &) = delete;
   ~Result() { Py_XDECREF(object); }
-  void make(PyObject *out, const char *key, at::ScalarType dtype, at::IntArrayRef shape, int dev) {
+  void make(PyObject *out, const char *key, at::ScalarType dtype, at::IntArrayRef shape, const Stream &on) {
+    const int dev = on.device();
     PyObject *given = out == Py_None ? nullptr : PyDict_GetItemString(out, key);
     if (given && given != Py_None) {
       data = like(given, (std::string("out['") + key + "']").c_str(), dtype, shape, dev);
@@ -121,11 +157,11 @@ struct Result {
     } else {
       at::Tensor t = at::empty(shape, at::TensorOptions(dtype).device(at::kCUDA, (c10::DeviceIndex)dev));
       data = t.data_ptr();
-      object = THPVariable_Wrap(std::move(t));
-      if (!object) throw Refused();
+      object = on.hand_out(std::move(t));
     }
   }
-  void status(PyObject *given, int dev) {
+  void status(PyObject *given, const Stream &on) {
+    const int dev = on.device();
     if (given != Py_None) {
       data = like(given, "status", at::kInt, {1}, dev);
       Py_INCREF(given);
@@ -133,8 +169,7 @@ struct Result {
     } else {
       at::Tensor t = at::zeros({1}, at::TensorOptions(at::kInt).device(at::kCUDA, (c10::DeviceIndex)dev));
       data = t.data_ptr();
-      object = THPVariable_Wrap(std::move(t));
-      if (!object) throw Refused();
+      object = on.hand_out(std::move(t));
     }
   }
 };
@@ -150,7 +185,6 @@ PyObject *answer(std::initializer_list<std::pair<const char *, const Result *>> 
   return d;
 }
 
-void *address(PyObject *o) { return o == Py_None ? nullptr : PyLong_AsVoidPtr(o); }
 int64_t whole(PyObject *o) {
   const int64_t v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw Refused();
@@ -163,11 +197,6 @@ double real(PyObject *o) {
 }
 void out_is_dict(PyObject *out) {
   if (out != Py_None && !PyDict_Check(out)) refuse(PyExc_TypeError, "out must be a dict");
-}
-
-// The given stream's address, or the device's current stream.
-void *stream_of(PyObject *o, int dev) {
-  return o == Py_None ? (void *)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream() : address(o);
 }
 
 // No C++ exception leaves a function of the module.
@@ -197,6 +226,7 @@ PyObject *norm_rope(PyObject *const *v) {
   if (q.dim() != 3) refuse(PyExc_ValueError, "q must be [rows, heads, D]");
   const int64_t rows = q.size(0), hq = q.size(1), d = q.size(2);
   const int dev = q.get_device();
+  const Stream on(v[9], dev);
   const at::ScalarType dt = q.scalar_type();
   out_is_dict(v[7]);
   if (d < 16 || d > 256 || d % 16) refuse(PyExc_ValueError, "head dimension must be a multiple of 16 to 256, got " + std::to_string(d));
@@ -208,18 +238,18 @@ PyObject *norm_rope(PyObject *const *v) {
     const at::Tensor &k = cuda_tensor(v[1], "k");
     hkv = k.dim() == 3 ? k.size(1) : -1;
     kh = heads(v[1], "k", dt, rows, hkv, d, dev);
-    ko.make(v[7], "k", dt, {rows, hkv, d}, dev);
+    ko.make(v[7], "k", dt, {rows, hkv, d}, on);
   }
-  qo.make(v[7], "q", dt, {rows, hq, d}, dev);
+  qo.make(v[7], "q", dt, {rows, hq, d}, on);
   const dspark_rope *rope = rope_for(v[3], d);
   const int32_t *pos = nullptr;
   if (rope || v[2] != Py_None) pos = like<int32_t>(v[2], "positions", at::kInt, {rows}, dev);
   const void *wq = weight(v[4], "q_weight", dt, d, dev), *wk = weight(v[5], "k_weight", dt, d, dev);
-  st.status(v[8], dev);
+  st.status(v[8], on);
   if (rows) {
     const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
     const int e = api.norm_rope(&qh, v[1] == Py_None ? nullptr : &kh, rows, (int32_t)hq, (int32_t)hkv, (int32_t)d, code, pos,
-                                rope, wq, wk, (float)real(v[6]), qo.data, ko.data, (int32_t *)st.data, stream_of(v[9], dev));
+                                rope, wq, wk, (float)real(v[6]), qo.data, ko.data, (int32_t *)st.data, on.raw());
     if (e) return PyLong_FromLong(e);
   }
   return answer({{"q", &qo}, {"k", &ko}, {"status", &st}});
@@ -229,6 +259,7 @@ PyObject *norm_rope(PyObject *const *v) {
 PyObject *append(PyObject *const *v) {
   const auto *cache = (const dspark_cache *)address(v[0]);
   const int dev = (int)whole(v[1]);
+  const Stream on(v[15], dev);
   const at::Tensor &k = cuda_tensor(v[2], "k");
   const int code = dtype_code(k, "k", {at::kFloat, at::kBFloat16, at::kHalf});
   const at::ScalarType dt = k.scalar_type();
@@ -243,16 +274,16 @@ PyObject *append(PyObject *const *v) {
     const at::Tensor &q = cuda_tensor(v[10], "q");
     hq = q.dim() == 3 ? q.size(1) : -1;
     qh = heads(v[10], "q", dt, rows, hq, d, dev);
-    qo.make(v[13], "q", dt, {rows, hq, d}, dev);
+    qo.make(v[13], "q", dt, {rows, hq, d}, on);
   }
   const dspark_rope *rope = rope_for(v[8], d);
   const int32_t *pos = maybe<int32_t>(v[7], "positions", at::kInt, {rows}, dev);
   const void *wk = weight(v[9], "k_weight", dt, d, dev), *wq = weight(v[11], "q_weight", dt, d, dev);
-  st.status(v[14], dev);
+  st.status(v[14], on);
   if (rows) {
     const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
     const int e = api.append(&kh, &vh, qo.data ? &qh : nullptr, (int32_t)hq, code, cache, &where, pos, rope, wq, wk,
-                             (float)real(v[12]), qo.data, (int32_t *)st.data, stream_of(v[15], dev));
+                             (float)real(v[12]), qo.data, (int32_t *)st.data, on.raw());
     if (e) return PyLong_FromLong(e);
   }
   return answer({{"q", &qo}, {"status", &st}});
@@ -262,19 +293,20 @@ PyObject *append(PyObject *const *v) {
 PyObject *read(PyObject *const *v) {
   const auto *cache = (const dspark_cache *)address(v[0]);
   const int dev = (int)whole(v[1]);
+  const Stream on(v[8], dev);
   const int64_t rows = whole(v[5]), d = cache->head_dim, h = cache->kv_heads;
   if (rows < 0) refuse(PyExc_ValueError, "rows must not be negative");
   out_is_dict(v[6]);
   const dspark_ragged where = ragged(v[2], v[3], v[4], rows, dev);
   Result k, ks, vo, vs, st;
-  k.make(v[6], "k", at::kFloat8_e4m3fn, {rows, h, d}, dev);
-  ks.make(v[6], "k_scale", at::kFloat8_e4m3fn, {rows, h, d / 16}, dev);
-  vo.make(v[6], "v", at::kFloat8_e4m3fn, {rows, h, d}, dev);
-  vs.make(v[6], "v_scale", at::kFloat8_e4m3fn, {rows, h, d / 16}, dev);
-  st.status(v[7], dev);
+  k.make(v[6], "k", at::kFloat8_e4m3fn, {rows, h, d}, on);
+  ks.make(v[6], "k_scale", at::kFloat8_e4m3fn, {rows, h, d / 16}, on);
+  vo.make(v[6], "v", at::kFloat8_e4m3fn, {rows, h, d}, on);
+  vs.make(v[6], "v_scale", at::kFloat8_e4m3fn, {rows, h, d / 16}, on);
+  st.status(v[7], on);
   if (rows) {
     const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
-    const int e = api.read(cache, &where, k.data, ks.data, vo.data, vs.data, (int32_t *)st.data, stream_of(v[8], dev));
+    const int e = api.read(cache, &where, k.data, ks.data, vo.data, vs.data, (int32_t *)st.data, on.raw());
     if (e) return PyLong_FromLong(e);
   }
   return answer({{"k", &k}, {"k_scale", &ks}, {"v", &vo}, {"v_scale", &vs}, {"status", &st}});
@@ -285,6 +317,7 @@ PyObject *paged(PyObject *const *v) {
   const at::Tensor &q = cuda_tensor(v[0], "q");
   const auto *cache = (const dspark_cache *)address(v[1]);
   const int dev = (int)whole(v[2]), code = dtype_code(q, "q", {at::kBFloat16, at::kHalf});
+  const Stream on(v[14], dev);
   if (q.dim() != 3) refuse(PyExc_ValueError, "q must be [rows, heads, D]");
   const at::ScalarType dt = q.scalar_type();
   const int64_t rows = q.size(0), hq = q.size(1), d = cache->head_dim, window = whole(v[8]);
@@ -296,9 +329,9 @@ PyObject *paged(PyObject *const *v) {
   const dspark_heads qh = heads(v[0], "q", dt, rows, hq, d, dev);
   const dspark_ragged where = ragged(v[3], v[4], v[5], rows, dev);
   Result o, lse, ws, st;
-  o.make(v[11], "out", dt, {rows, hq, d}, dev);
-  if (PyObject_IsTrue(v[10])) lse.make(v[11], "lse", at::kFloat, {rows, hq}, dev);
-  st.status(v[13], dev);
+  o.make(v[11], "out", dt, {rows, hq, d}, on);
+  if (PyObject_IsTrue(v[10])) lse.make(v[11], "lse", at::kFloat, {rows, hq}, on);
+  st.status(v[13], on);
   if (rows) {
     const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
     const int64_t need = (int64_t)api.workspace_bytes((int32_t)hq, cache, &where, max_rows);
@@ -314,13 +347,13 @@ PyObject *paged(PyObject *const *v) {
         }
       }
       if (!ws.data) {
-        ws.make(Py_None, "workspace", at::kByte, {need}, dev);
+        ws.make(Py_None, "workspace", at::kByte, {need}, on);
         have = need;
       }
     }
     const double scale = v[6] == Py_None ? 1.0 / std::sqrt((double)d) : real(v[6]);
     const int e = api.paged(&qh, (int32_t)hq, code, cache, &where, max_rows, (float)scale, PyObject_IsTrue(v[7]), window, o.data,
-                            (float *)lse.data, ws.data, (size_t)have, (int32_t *)st.data, stream_of(v[14], dev));
+                            (float *)lse.data, ws.data, (size_t)have, (int32_t *)st.data, on.raw());
     if (e) return PyLong_FromLong(e);
   }
   return answer({{"out", &o}, {"lse", &lse}, {"status", &st}, {"workspace", &ws}});
@@ -333,6 +366,7 @@ PyObject *penalize(PyObject *const *v) {
   if (z.dim() != 2) refuse(PyExc_ValueError, "logits must be [rows, V]");
   const int64_t rows = z.size(0), V = z.size(1);
   const int dev = z.get_device();
+  const Stream on(v[14], dev);
   out_is_dict(v[12]);
   const void *in = like(v[0], "logits", z.scalar_type(), {rows, V}, dev);
   const at::Tensor &hist = cuda_tensor(v[2], "hist");
@@ -359,11 +393,11 @@ PyObject *penalize(PyObject *const *v) {
   p.bias_val = maybe<float>(v[10], "bias_val", at::kFloat, {B, p.bias_cap}, dev);
   p.mask = maybe(v[11], "mask", at::kInt, {rows, (V + 31) / 32}, dev);
   Result o, st;
-  o.make(v[12], "logits", z.scalar_type(), {rows, V}, dev);
-  st.status(v[13], dev);
+  o.make(v[12], "logits", z.scalar_type(), {rows, V}, on);
+  st.status(v[13], on);
   if (rows) {
     const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
-    const int e = api.penalize(in, code, rows, V, B, off, &p, o.data, (int32_t *)st.data, stream_of(v[14], dev));
+    const int e = api.penalize(in, code, rows, V, B, off, &p, o.data, (int32_t *)st.data, on.raw());
     if (e) return PyLong_FromLong(e);
   }
   return answer({{"logits", &o}, {"status", &st}});

@@ -4,8 +4,9 @@ key/value cache held in 4 bits, attention over it, and the penalties, biases and
 All take the ragged rows of the scheduler and the verification: request r owns rows row_off[r] ..
 row_off[r+1]-1 (``tgt_off``), the last of its kv_len[r] tokens.  The functions here name the arguments;
 csrc/binding.cpp checks them, allocates outputs and workspaces with torch and calls the C ABI on the
-current stream (a kernel may take 3 us: the same checks in Python took 13 us a call).  Nothing is
-synchronised.  Pass ``status`` (one int32 on the device, see ``check``) to share the error word
+current stream (a kernel may take 3 us: the same checks in Python took 13 us a call), or on ``stream``,
+where it is given: what the call allocates belongs to that stream then, and its inputs have to be ready
+there and stay until it is done with them.  Nothing is synchronised.  Pass ``status`` (one int32 on the device, see ``check``) to share the error word
 of a step; without it each call makes its own.
 """
 from __future__ import annotations

@@ -1,5 +1,5 @@
 """The operators around a ragged verification step where they once went wrong: norm weights off their boundary, NaN in
-16-bit keys and values, elements and scales at the borders of their codes."""
+16-bit keys and values, elements and scales at the borders of their codes, calls on a stream of their own."""
 import math
 
 import pytest
@@ -152,3 +152,70 @@ def test_norm_weights_off_a_boundary_are_refused():
                 ds.norm_rope(q, q, **kw)
             with pytest.raises(ValueError, match="16-byte"):
                 ds.cache_append(cache, q, q, *where, q=q, **kw)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# streams and failed steps
+# ---------------------------------------------------------------------------------------------------------------
+def each_operator(seed=48, kv=(50, 20)):
+    """name -> (call(**kw), its outputs' names) of every operator, on inputs of its own."""
+    g, n, d, page = gen(seed), [3, 1], 64, 16
+    table, pages = paged(g, list(kv), page)
+    cache, _ = filled(g, list(kv), table, pages, 2, d, page)
+    x = randn(g, 4, 8, d).bfloat16()
+    rope, off, lens = ds.Rope(d), offsets(n), i32(list(kv))
+    one, z = torch.full((2,), 1.5, device="cuda"), randn(g, 4, 999)
+    hist, two, pos = i32([[1, 2, 3], [4, 5, 998]]), i32([2, 3]), i32([5, 6, 7, 8])
+    return {
+        "norm_rope": (lambda **kw: ds.norm_rope(x[:, :4], x[:, 4:6], pos, rope, **kw), ("q", "k")),
+        "cache_append": (lambda **kw: ds.cache_append(cache, x[:, 4:6], x[:, 6:], off, lens, table, rope=rope,
+                                                      q=x[:, :4], **kw), ("q",)),
+        "cache_read": (lambda **kw: ds.cache_read(cache, off, lens, table, 4, **kw), ("k", "k_scale", "v", "v_scale")),
+        "attend_paged": (lambda **kw: ds.attend_paged(x[:, :4], cache, off, lens, table, max_rows=3, want_lse=True, **kw),
+                         ("out", "lse")),
+        "penalize_logits": (lambda **kw: ds.penalize_logits(z, off, hist, two, two, one, one, one, **kw), ("logits",)),
+    }
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8).clone()
+
+
+@pytest.mark.parametrize("name", ["norm_rope", "cache_append", "cache_read", "attend_paged", "penalize_logits"])
+def test_a_stream_of_its_own_while_the_current_one_is_busy(name):
+    call, outputs = each_operator()[name]
+    want = call()
+    ok(want["status"])
+    words = [torch.full((1,), 8, dtype=torch.int32, device="cuda") for _ in range(256)]   # freed words that hold an error
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    del words[::2]
+    torch.cuda._sleep(200_000_000)                          # a tenth of a second that the current stream has to do
+    got = call(stream=side)
+    with torch.cuda.stream(side):
+        kept = {h: bits(got[h]) for h in outputs}
+    assert ds.check(got["status"], stream=side) == "DSPARK_OK"
+    side.synchronize()
+    for h in outputs:
+        assert torch.equal(kept[h], bits(want[h]))
+
+
+def test_a_result_dropped_at_once_keeps_its_memory_until_its_stream_is_done():
+    g, d, kv = gen(49), 128, [60000]
+    table, pages = paged(g, kv, 64)
+    cache, _ = filled(g, kv, table, pages, 1, d, 64)
+    q, off, lens = randn(g, 1, 8, d).bfloat16(), offsets([1]), i32(kv)
+    want = ds.attend_paged(q, cache, off, lens, table)
+    size = want["workspace"].numel()
+    side, out = torch.cuda.Stream(), torch.empty_like(want["out"])
+    want = want["out"].clone()
+    for _ in range(5):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        ds.attend_paged(q, cache, off, lens, table, out=dict(out=out), stream=side)      # its workspace is dropped here
+        for _ in range(4000):                                  # the current stream takes what memory is free
+            torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        side.synchronize()
+        assert torch.equal(out, want)
