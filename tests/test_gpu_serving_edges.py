@@ -1,5 +1,6 @@
 """The operators around a ragged verification step where they once went wrong: norm weights off their boundary, NaN in
-16-bit keys and values, elements and scales at the borders of their codes, calls on a stream of their own."""
+16-bit keys and values, elements and scales at the borders of their codes, windows past every token, calls on a
+stream of their own."""
 import math
 
 import pytest
@@ -152,6 +153,25 @@ def test_norm_weights_off_a_boundary_are_refused():
                 ds.norm_rope(q, q, **kw)
             with pytest.raises(ValueError, match="16-byte"):
                 ds.cache_append(cache, q, q, *where, q=q, **kw)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# what a row sees
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_window_past_every_token_is_none(d, causal):
+    g, n, kv = gen(45), [5, 12, 2], [2, 7, 90]               # two requests with rows before their first token
+    table, pages = paged(g, kv, 16)
+    cache, held = filled(g, kv, table, pages, 1, d, 16)
+    q = randn(g, sum(n), 3, d).bfloat16()
+    args = (q, cache, offsets(n), i32(kv), table)
+    want = ds.attend_paged(*args, causal=causal, want_lse=True)
+    attend_check(q, want, held, n, kv, d ** -0.5, causal, 0)
+    for window in (90, 2 ** 30, 2 ** 31 - 12, 2 ** 31 - 3, 2 ** 31 - 1):
+        got = ds.attend_paged(*args, causal=causal, window=window, want_lse=True)
+        ok(got["status"])
+        assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"]), window
 
 
 # ---------------------------------------------------------------------------------------------------------------
