@@ -483,7 +483,8 @@ typedef struct {
 
 /* Ragged rows over the cache.  row_off [B+1] int32; kv_len [B] int32, a request's tokens in the
  * cache with this step's rows among them; page_table [B, max_pages] int32 page ids, entries past a
- * request's last page are not read, max_pages * page_size < 2^31; rows: the rows of the call's tensors, >= row_off[B].
+ * request's last page are not read, and the attention with a window does not read those of pages that lie before
+ * every row's window; max_pages * page_size < 2^31; rows: the rows of the call's tensors, >= row_off[B].
  * Row j of request r is token kv_len[r] - n_r + j, n_r = row_off[r+1] - row_off[r]. */
 typedef struct {
   const int32_t *row_off, *kv_len, *page_table;

@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT, D))
   const int32_t *table = a.table + r * a.max_pages;
   const int tiles_per_page = a.page_size / kTileTokens;
   int32_t page = -1;
+  bool gone = false;
   {
     const bool whole = tiles_per_page % TC == 0;
     const int per_page = whole ? tiles_per_page / TC : tiles_per_page, per_step = whole ? 1 : TC;
@@ -257,16 +258,19 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT, D))
     if (lane < TC) {
       const int piece = lane < per_step ? per_step * (c0 + w0) + lane : 0x3fffffff;
       places[warp * TC + lane] = make_int4(piece, piece / per_page, piece % per_page, 0);
-      if (w0 < chunks && piece < pieces) page = table[piece / per_page];
+      // The first step may hold tiles that lie before the window altogether.  Their pages may be gone: they are not
+      // looked up.
+      gone = !whole && piece < lo_min / kTileTokens;
+      if (w0 < chunks && !gone && piece < pieces) page = table[piece / per_page];
     }
     __syncthreads();
   }
-  auto issue = [&](int c, int stage) {       // chunk c, and the look-up for chunk c + step
+  auto issue = [&](int c, int stage, bool gone) {       // chunk c, and the look-up for chunk c + step
     if (lane < TC) {
       constexpr uint32_t kLanes = (1u << TC) - 1;
       const int4 by = fixed[0], k = fixed[1];
       int4 at = places[warp * TC + lane];
-      const bool want = at.x < k.y, ok = want && page >= 0 && page < a.pages;
+      const bool want = at.x < k.y && !gone, ok = want && page >= 0 && page < a.pages;
       if (want && !ok) set_status(a.dev_status, DSPARK_ERR_PAGES);
       const uint32_t got = __ballot_sync(kLanes, ok);
       if (lane == 0) mbar_arrive_tx(bar + 8 * stage, __popc(got) * k.x);
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT, D))
   };
 #pragma unroll
   for (int i = 0; i < kStages; ++i)
-    if (w0 + i * step < chunks) issue(w0 + i * step, i);
+    if (w0 + i * step < chunks) issue(w0 + i * step, i, i == 0 && gone);
 
   // Queries, an n-tile a warp: a lane has row g, dimensions [q4 D/4, (q4 + 1) D/4).
   if (warp < NT) {
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT, D))
       step_on(buf, base, std::false_type());
     __syncwarp();
     const int next = c + kStages * step;
-    if (next < chunks) issue(next, stage);
+    if (next < chunks) issue(next, stage, false);
     if (++stage == kStages) {
       stage = 0;
       phase ^= 1;

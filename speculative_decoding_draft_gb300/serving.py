@@ -253,7 +253,8 @@ def attend_paged(q, cache: PagedCache, row_off, kv_len, page_table, *, scale: Op
 
     q [rows, Hq, D] bfloat16 or float16 (rows and heads may be strided), Hq a multiple of the cache's heads;
     scale: 1/sqrt(D) unless given.  Row j of request r sees its tokens up to itself (causal) or all kv_len[r], and
-    with window > 0 only the last ``window`` of them; a row that sees nothing gets 0 and lse -inf.  max_rows: the
+    with window > 0 only the last ``window`` of them (pages before every row's window may be gone: their entries in
+    page_table are not read); a row that sees nothing gets 0 and lse -inf.  max_rows: the
     most rows of a request (default: what ``rows`` allows; smaller is faster).  Returns out [rows, Hq, D] and,
     with want_lse, lse [rows, Hq] float32.
     """

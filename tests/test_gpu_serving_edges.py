@@ -1,6 +1,6 @@
 """The operators around a ragged verification step where they once went wrong: norm weights off their boundary, NaN in
-16-bit keys and values, elements and scales at the borders of their codes, windows past every token, calls on a
-stream of their own."""
+16-bit keys and values, elements and scales at the borders of their codes, windows past every token, pages that a
+window has left, calls on a stream of their own."""
 import math
 
 import pytest
@@ -172,6 +172,45 @@ def test_a_window_past_every_token_is_none(d, causal):
         got = ds.attend_paged(*args, causal=causal, window=window, want_lse=True)
         ok(got["status"])
         assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"]), window
+
+
+@pytest.mark.parametrize("d,page,n,window,causal", [
+    (128, 16, 1, 20, True), (64, 16, 3, 33, True), (64, 32, 2, 1, True), (128, 48, 7, 17, True), (64, 48, 5, 40, False),
+    (128, 64, 2, 30, True), (128, 16, 30, 9, True)])
+def test_pages_that_the_window_has_left_are_not_looked_up(d, page, n, window, causal):
+    g, kv = gen(46 + d + page), list(range(40, 300, 13))
+    B, rows = len(kv), [n] * len(kv)
+    table, pages = paged(g, kv, page)
+    cache, held = filled(g, kv, table, pages, 2, d, page)
+    q = randn(g, sum(rows), 4, d).half()
+    args = dict(causal=causal, window=window, max_rows=n, want_lse=True)
+    want = ds.attend_paged(q, cache, offsets(rows), i32(kv), table, **args)
+    ok(want["status"])
+    freed = table.clone()
+    for r in range(B):
+        first = max(0, (kv[r] - n + 1 if causal else kv[r]) - window)       # the first token that a row sees
+        freed[r, : first // page] = -1
+    assert (freed != table).any()
+    got = ds.attend_paged(q, cache, offsets(rows), i32(kv), freed, **args)
+    ok(got["status"])
+    assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+    attend_check(q, got, held, rows, kv, d ** -0.5, causal, window)
+    freed[0, (kv[0] - 1) // page] = pages                 # one that a row does see
+    bad = ds.attend_paged(q, cache, offsets(rows), i32(kv), freed, **args)["status"]
+    assert ds.check(bad) == "DSPARK_ERR_PAGES"
+
+
+def test_pages_that_the_window_has_left_of_a_request_in_parts():
+    g, d, page, kv, window = gen(47), 128, 16, [60007], 39985
+    table, pages = paged(g, kv, page)
+    cache, held = filled(g, kv, table, pages, 1, d, page)
+    q = randn(g, 2, 4, d).bfloat16()
+    freed = table.clone()
+    freed[0, : (kv[0] - 1 - window) // page] = -1
+    got = ds.attend_paged(q, cache, offsets([2]), i32(kv), freed, window=window, want_lse=True)
+    ok(got["status"])
+    assert got["workspace"] is not None
+    attend_check(q, got, held, [2], kv, d ** -0.5, True, window)
 
 
 # ---------------------------------------------------------------------------------------------------------------
