@@ -222,8 +222,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT, D))
   const int ctx = (int)(kv - n);
   const int hi_min = a.causal ? ctx + first / a.group + 1 : (int)kv;
   const int hi_max = a.causal ? ctx + last / a.group + 1 : (int)kv;
-  auto start_of = [&](int hi) { return a.window && hi > a.window ? hi - a.window : 0; };   // hi may be negative
-  const int lo_min = start_of(hi_min), lo_max = start_of(hi_max);
+  // (ends may be negative: what is subtracted from is the larger of end and window)
+  const int lo_min = a.window ? max(hi_min, a.window) - a.window : 0;
+  const int lo_max = a.window ? max(hi_max, a.window) - a.window : 0;
   const int c0 = lo_min / kChunk;
   const int chunks = skip || hi_max <= 0 ? 0 : (hi_max + kChunk - 1) / kChunk - c0;
 
