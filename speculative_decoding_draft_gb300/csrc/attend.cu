@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT, D))
     if (tid == 0) {
       fixed[0] = make_int4(ahead, ahead / per_page, ahead % per_page, per_page);
       fixed[1] = make_int4(whole ? TC * tile_bytes(D) : tile_bytes(D), pieces, h, chunks);
-      fixed[2] = make_int4((int)row0, total, first, 0);
+      fixed[2] = make_int4((int)row0, skip ? 0 : total, first, 0);      // no rows to store where the step had failed
     }
     if (lane < TC) {
       const int piece = lane < per_step ? per_step * (c0 + w0) + lane : 0x3fffffff;

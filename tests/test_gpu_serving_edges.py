@@ -1,6 +1,6 @@
 """The operators around a ragged verification step where they once went wrong: norm weights off their boundary, NaN in
 16-bit keys and values, elements and scales at the borders of their codes, windows past every token, pages that a
-window has left, calls on a stream of their own."""
+window has left, calls on a stream of their own, steps that had failed before the call."""
 import math
 
 import pytest
@@ -278,3 +278,24 @@ def test_a_result_dropped_at_once_keeps_its_memory_until_its_stream_is_done():
             torch.full((size,), 255, dtype=torch.uint8, device="cuda")
         side.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("name", ["norm_rope", "cache_append", "cache_read", "attend_paged", "penalize_logits"])
+def test_a_step_that_failed_leaves_the_outputs_alone(name):
+    call, outputs = each_operator()[name]
+    good = call()
+    out = {h: torch.full_like(good[h], 3.0) for h in outputs}
+    st = i32([8])
+    call(status=st, out=out)
+    assert ds.check(st) == "DSPARK_ERR_LENGTHS"
+    assert all((out[h].float() == 3).all() for h in outputs)
+
+
+def test_a_step_that_failed_leaves_attention_in_parts_alone():
+    g, d, kv = gen(50), 64, [40000]
+    table, pages = paged(g, kv, 64)
+    cache, _ = filled(g, kv, table, pages, 1, d, 64)
+    q, out = randn(g, 2, 2, d).half(), dict(out=torch.full((2, 2, d), 3.0, device="cuda").half())
+    st = i32([8])
+    got = ds.attend_paged(q, cache, offsets([2]), i32(kv), table, out=out, status=st)
+    assert got["workspace"] is not None and ds.check(st) == "DSPARK_ERR_LENGTHS" and (out["out"] == 3).all()
