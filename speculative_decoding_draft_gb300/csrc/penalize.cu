@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads, DT == DSPARK_F32 ? 4 : 5) penalize_k
   using T = typename Elem<DT>::T;
   constexpr int N = 16 / sizeof(T);           // elements of a piece
   constexpr uint32_t kAll = (1u << N) - 1;
-  extern __shared__ uint32_t counts[];        // [slice]
+  extern __shared__ __align__(16) uint32_t counts[];        // [slice], cleared 16 bytes at a time
   uint32_t *map = counts + slice;             // [slice / 32]: listed tokens
   Bias *biases = reinterpret_cast<Bias *>(map + slice / 32);                        // [bias_cap], in no order
   uint16_t *list = reinterpret_cast<uint16_t *>(biases + a.bias_cap);               // [slice]
