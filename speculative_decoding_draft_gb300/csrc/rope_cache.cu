@@ -30,7 +30,7 @@ namespace {
 
 // Ring of a warp and CTAs an SM: the append, with more to compute, wants warps rather than bytes under way.
 constexpr int ring_bytes(bool append) { return append ? 4096 : 6144; }
-constexpr int kEnoughWarps = 2048;
+constexpr int kEnoughWarps = 2048; // 13 on each of 152 SMs, under half of those that fit there together
 constexpr int kWarps = 4;          // of a CTA; they share nothing
 
 using Pair = unsigned long long;   // two fp32
@@ -394,25 +394,28 @@ __global__ void __launch_bounds__(kWarps * 32, 16) read_kernel(const __grid_cons
 
 template <int DT, int LANES, bool APPEND>
 cudaError_t launch_lanes(const HeadsArgs &a, cudaStream_t s) {
-  // a row's heads in shares as long as the rows alone leave the SMs without work: 24 warps on each of
-  // 152 and several rounds of them
+  // a row's heads in shares as long as the rows alone make fewer than kEnoughWarps warps
   int log_parts = 0;
   const int most = (a.Hq + (APPEND ? 2 : 1) * a.Hkv) * LANES / 64;      // chunks
   while ((a.rows << log_parts) < kEnoughWarps && 2 << log_parts <= most) ++log_parts;
   const int64_t jobs = a.rows << log_parts;
   const unsigned grid = (unsigned)((jobs + kWarps - 1) / kWarps);
-  if (a.D == 8 * LANES)
-    heads_kernel<DT, LANES, true, APPEND><<<grid, kWarps * 32, 0, s>>>(a, log_parts);
-  else
-    heads_kernel<DT, LANES, false, APPEND><<<grid, kWarps * 32, 0, s>>>(a, log_parts);
+  if constexpr (APPEND) {
+    heads_kernel<DT, LANES, true, true><<<grid, kWarps * 32, 0, s>>>(a, log_parts);
+  } else {
+    if (a.D == 8 * LANES)
+      heads_kernel<DT, LANES, true, false><<<grid, kWarps * 32, 0, s>>>(a, log_parts);
+    else
+      heads_kernel<DT, LANES, false, false><<<grid, kWarps * 32, 0, s>>>(a, log_parts);
+  }
   return cudaGetLastError();
 }
 
 template <int DT, bool APPEND>
 cudaError_t launch_heads(const HeadsArgs &a, cudaStream_t s) {
-  if (a.D <= 64) return launch_lanes<DT, 8, APPEND>(a, s);
-  if (a.D <= 128) return launch_lanes<DT, 16, APPEND>(a, s);
-  return launch_lanes<DT, 32, APPEND>(a, s);
+  if constexpr (!APPEND)                     // the cache holds heads of 64 and 128 dimensions
+    if (a.D > 128) return launch_lanes<DT, 32, false>(a, s);
+  return a.D <= 64 ? launch_lanes<DT, 8, APPEND>(a, s) : launch_lanes<DT, 16, APPEND>(a, s);
 }
 
 template <bool APPEND>
