@@ -14,6 +14,7 @@ S3.2.2 Algorithm 1).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -151,6 +152,27 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _on_its_stream(fn):
+    """A call with ``stream=`` has that stream as the current one: what it allocates, the fill of its status word and
+    its kernels follow one another there, and memory that the caller drops at once is not used again before they are
+    done.  What it returns counts as used by the caller's current stream too."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        before = torch.cuda.current_stream()
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            r = fn(*args, **kw)
+        for t in (r if isinstance(r, dict) else vars(r)).values():
+            if isinstance(t, torch.Tensor):
+                t.record_stream(before)
+        return r
+    return call
+
+
 def _dev(t: torch.Tensor, name: str, dtype=None, shape=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -210,6 +232,7 @@ class PackedProjection:
         self.device = data.device
 
 
+@_on_its_stream
 def pack_projection(W, *, stream=None) -> PackedProjection:
     """Pack W2 [rank, V] bfloat16 once for the tensor-core draft path."""
     _dev(W, "W", torch.bfloat16)
@@ -239,6 +262,7 @@ def new_status(device) -> torch.Tensor:
 # ---------------------------------------------------------------------------
 # entry points
 # ---------------------------------------------------------------------------
+@_on_its_stream
 def draft_markov_sample(U, E, W, anchor, K_r, temperature, seed: int, *, want_logits: bool = True,
                         want_lse: bool = True, want_tok_logit: bool = True, force_simt: bool = False,
                         spare_sm: bool = False,
@@ -316,6 +340,7 @@ def draft_markov_sample(U, E, W, anchor, K_r, temperature, seed: int, *, want_lo
                 workspace=ws)
 
 
+@_on_its_stream
 def draft_rnn_sample(U, E, W, rnn_W, rnn_x, anchor, K_r, temperature, seed: int, *, want_logits: bool = True,
                      want_lse: bool = True, want_tok_logit: bool = True, out: Optional[dict] = None,
                      workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
@@ -354,6 +379,7 @@ def draft_rnn_sample(U, E, W, rnn_W, rnn_x, anchor, K_r, temperature, seed: int,
     return dict(draft_tok=tok, draft_logits=logits, draft_lse=lse, draft_tok_logit=zx, status=status, workspace=ws)
 
 
+@_on_its_stream
 def schedule_survival(conf, K_r, sps, *, out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
                       status: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Hardware-aware prefix scheduler (C ABI dspark_schedule_survival).
@@ -388,6 +414,7 @@ def _out(out, key, shape, dtype, dev):
     return t if t is not None else torch.empty(shape, dtype=dtype, device=dev)
 
 
+@_on_its_stream
 def schedule_capacity(conf, K_r, sps, *, out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
                       status: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Capacity of the asynchronous scheduler (C ABI dspark_schedule_capacity).
@@ -415,6 +442,7 @@ def schedule_capacity(conf, K_r, sps, *, out: Optional[dict] = None, workspace: 
     return dict(capacity=cap, theta_best=th, ell=ell, tgt_off=off, status=status, workspace=ws)
 
 
+@_on_its_stream
 def schedule_topk(conf, K_r, capacity, *, out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
                   status: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Dynamic top-K admission (C ABI dspark_schedule_topk); capacity is a CUDA int32 [1] tensor."""
@@ -440,6 +468,7 @@ def schedule_topk(conf, K_r, capacity, *, out: Optional[dict] = None, workspace:
 THRESHOLD_CONFIDENCE, THRESHOLD_SURVIVAL = 0, 1
 
 
+@_on_its_stream
 def schedule_threshold(conf, K_r, threshold: float, mode: int = THRESHOLD_CONFIDENCE, *,
                        out: Optional[dict] = None, status: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Static-threshold lengths (C ABI dspark_schedule_threshold)."""
@@ -460,6 +489,7 @@ def schedule_threshold(conf, K_r, threshold: float, mode: int = THRESHOLD_CONFID
     return dict(ell=ell, tgt_off=off, b_star=bs, survival=surv, status=status)
 
 
+@_on_its_stream
 def verify_ragged(draft_logits, tgt_logits, tgt_off, ell, draft_tok, temperature, seed: int, *,
                   draft_lse=None, out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
                   status: Optional[torch.Tensor] = None, stream=None) -> dict:
@@ -502,6 +532,7 @@ def verify_markov_workspace_bytes(B: int, K_max: int, V: int, rank: int, packed:
                                                                 FLAG_W_PACKED if packed else 0)))
 
 
+@_on_its_stream
 def verify_markov(U, E, W, anchor, draft_lse, draft_tok_logit, tgt_logits, tgt_off, ell, draft_tok, temperature,
                   seed: int, *, out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
                   status: Optional[torch.Tensor] = None, stream=None) -> dict:
