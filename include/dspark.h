@@ -502,7 +502,8 @@ dspark_status dspark_attn_norm_rope(const dspark_heads *q, const dspark_heads *k
 
 /* Append k and v [rows, kv_heads, D] to the cache: keys normed and rotated as above, then both
  * quantised: scale = e4m3(max |y| / 6) over 16 dimensions of y / k_scale (or v_scale), element =
- * e2m1(y / scale), both to nearest, ties to even, saturating; a group with a NaN gets the scale NaN.
+ * e2m1(y / scale), both to the nearest of y in fp32, ties to even, saturating; a group with a NaN gets the
+ * scale NaN and elements 0.
  * With q [rows, q_heads, D] the queries are normed and rotated in the same pass into q_out.
  * positions NULL: a row's rotary position is its place in the cache.  F32, BF16, F16.
  * Device errors: OFFSETS (row_off), LENGTHS (a row before token 0 or past the page table), PAGES. */
@@ -520,7 +521,7 @@ dspark_status dspark_attn_cache_read(const dspark_cache *cache, const dspark_rag
  * key/value head i / (q_heads / kv_heads).  Row j of request r sees tokens t < hi, hi = kv_len[r]
  * (causal: kv_len[r] - n_r + j + 1), and with window > 0 only t >= hi - window.  A row that sees
  * nothing gets 0 and lse -inf.  lse [rows, q_heads] float, optional: log sum exp(scale q.k).
- * max_rows: no request has more rows (sizes the launch; a larger one is DSPARK_ERR_LENGTHS).
+ * max_rows: no request has more rows (sizes the launch; a larger one is DSPARK_ERR_LENGTHS); at most 2^20.
  * BF16, F16.
  * workspace: >= dspark_attn_paged_workspace_bytes(the same arguments) bytes, 256-byte aligned; where that is
  * 0 (all but few requests with long tables) it may be NULL. */
@@ -539,7 +540,7 @@ typedef struct {
   const int32_t *prompt_len;         /* [B] how many of them are the prompt's                            */
   const int32_t *draft_tok;          /* [B, draft_cap] or NULL: row j counts draft tokens 0 .. j-1 as output */
   const float *repetition, *presence, *frequency;   /* [B]                                              */
-  const int32_t *bias_tok;           /* [B, bias_cap], -1 pads; a token listed twice gets the sum         */
+  const int32_t *bias_tok;           /* [B, bias_cap]; a token listed twice gets the sum; ids outside [0, V), as a padding -1, are left out */
   const float *bias_val;             /* [B, bias_cap]                                                   */
   const void *mask;                  /* [rows, (V+31)/32] 32-bit words or NULL: bit v%32 of word v/32 allows v */
   int64_t hist_cap, draft_cap, bias_cap;

@@ -37,9 +37,11 @@
 // rows a warp (90), 8 rows (104), two warps sharing a step of 32 rows with half of the output each (133), steps
 // of 16 tokens (84) and of 64 (86), chunks drawn from a counter instead of dealt (no faster, and not
 // reproducible).  The fifth-generation tensor cores take operands from shared or tensor memory only, where
-// every expanded element would have to be written and read again: 1 KB a token and head each way against the
-// 144 bytes that are stored, 3 times what shared memory can move in the time that the stored bytes take to
-// arrive.
+// every expanded element would have to be written and read again: 512 bytes a token and head each way (fp16, 128
+// dimensions) against the 144 that are stored.  At the memory's rate an SM receives 23 stored bytes a cycle, so
+// that is 83 bytes in and 83 out of shared memory's 128 a cycle: 1.3 times what it can move meanwhile, or 34 us
+// for the 64 requests if nothing else used it.  One expansion would then serve all row-heads of a key/value head,
+// which pays where there are many (prompts, whose tiles of 16 or 32 rows each expand the cache again).  Not built.
 #include <type_traits>
 
 #include <cooperative_groups.h>
@@ -128,8 +130,10 @@ __device__ __forceinline__ uint32_t lds_u8(const uint8_t *p) { return *p; }
 
 // The i-th request, long ones first: CTAs start in the order of their index, and one that starts last must
 // not be the longest (64 requests 85 us, 97 in the order given; 256 requests 266, 300).  Eight classes by
-// length; every warp works it out by itself from the lengths, as long as it can hold these (B <= 256; with
-// more requests the last CTAs weigh little).
+// length; every warp works it out by itself from the lengths, as long as it can hold these (B <= 256).  More
+// requests start in the order given, which costs less the more there are: of up to 4096 tokens with 1 to 8 rows
+// 300 take 332 us (314 if given longest first) and 512 take 534 (515), 2048 of up to 2048 tokens 1308 (1293);
+// with heads of 64 dimensions and 1 or 2 rows 512 of up to 16384 tokens take 505 (455).
 constexpr int kOrderMost = 256;
 __device__ __forceinline__ int64_t longest_first(const int32_t *kv_len, int64_t B, int64_t i, int lane) {
   if (B > kOrderMost || B < 2) return i;

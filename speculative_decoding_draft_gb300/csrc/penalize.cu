@@ -12,7 +12,7 @@
 // and lists every token that it may have to change (history, draft tokens, biases).  Then it goes over
 // the rows twice: all of the slice, 16 bytes at a time, with the mask alone; and the few listed
 // tokens, in what the first pass wrote.  (Changing them on the way, piece by piece, made the kernel
-// large and divergent: 260 us for 288 rows of 151936 where this takes 52.)  In place and without
+// large and divergent: 260 us for 288 rows of 151936 where this takes 54.)  In place and without
 // a mask the first pass has nothing to do.
 #include "attn.cuh"
 
