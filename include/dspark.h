@@ -533,6 +533,28 @@ dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t 
                                 int64_t window, void *out, float *lse, void *workspace, size_t workspace_bytes,
                                 int32_t *dev_status, void *stream);
 
+/* Attention of whole prompts: ragged rows over ragged keys and values in 16 bits.  Request r's queries are rows
+ * row_off[r] .. row_off[r+1]-1 of q [rows, q_heads, D] and its m_r tokens are rows kv_off[r] .. kv_off[r+1]-1 of k and
+ * v [kv_rows, kv_heads, D] (kv_off may be row_off; more tokens than queries: earlier pieces of the same prompt come
+ * first).  out [rows, q_heads, D] = softmax(scale q.k) v over the tokens that a row sees, query head i with key/value
+ * head i / (q_heads / kv_heads): row j of n_r sees tokens t < hi, hi = m_r (causal: m_r - n_r + j + 1), and with
+ * window > 0 only t >= hi - window.  A row that sees nothing gets 0 and lse -inf.  What masked tokens hold,
+ * infinities and NaN included, changes nothing.  lse [rows, q_heads] float, optional: log sum exp(scale q.k).
+ * row_off, kv_off [B+1] int32, not falling; rows of out at and past row_off[B] are left alone.  D 64 or 128; rows *
+ * q_heads / kv_heads < 2^31 - 256.  k and v have their heads inside the rows (all of a row's heads before the next
+ * row), or their rows inside the heads with the head's stride a multiple of the row's; no stride is 0 (broadcast).
+ * BF16, F16.
+ * workspace: >= dspark_attn_prompt_workspace_bytes(the same sizes) bytes, 256-byte aligned; where that is 0 (all
+ * but few queries over many tokens) it may be NULL.  Device errors: OFFSETS. */
+size_t dspark_attn_prompt_workspace_bytes(int64_t rows, int64_t kv_rows, int64_t B, int32_t q_heads, int32_t kv_heads,
+                                          int32_t head_dim);
+
+dspark_status dspark_attn_prompt(const dspark_heads *q, const dspark_heads *k, const dspark_heads *v, int64_t rows,
+                                 int64_t kv_rows, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                 int32_t dtype, const int32_t *row_off, const int32_t *kv_off, float scale,
+                                 int32_t causal, int64_t window, void *out, float *lse, void *workspace,
+                                 size_t workspace_bytes, int32_t *dev_status, void *stream);
+
 /* Penalties, biases and masks of the logits' rows. */
 typedef struct {
   const int32_t *hist;               /* [B, hist_cap] token ids: the prompt, then the output so far       */

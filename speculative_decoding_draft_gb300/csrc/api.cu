@@ -765,6 +765,57 @@ dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t 
   return launch_attend(a, (cudaStream_t)stream, dev.sms) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
+static dspark_status check_prompt(int64_t rows, int64_t kv_rows, int64_t B, int32_t q_heads, int32_t kv_heads,
+                                  int32_t head_dim) {
+  if (rows < 1 || rows > kMaxRows || kv_rows < 0 || kv_rows > kMaxRows - 128 || B < 1 || B > kMaxB || q_heads < 1 ||
+      q_heads > kMaxHeads || kv_heads < 1 || q_heads % kv_heads || rows * (q_heads / kv_heads) > kMaxRows - 256)
+    return DSPARK_ERR_DIMS;
+  return head_dim == 64 || head_dim == 128 ? DSPARK_OK : DSPARK_ERR_UNSUPPORTED;
+}
+
+size_t dspark_attn_prompt_workspace_bytes(int64_t rows, int64_t kv_rows, int64_t B, int32_t q_heads, int32_t kv_heads,
+                                          int32_t head_dim) {
+  DeviceInfo dev;
+  if (check_prompt(rows, kv_rows, B, q_heads, kv_heads, head_dim) != DSPARK_OK || !device_info(&dev)) return 0;
+  return (size_t)prompt_workspace_bytes(rows, kv_rows, B, q_heads, kv_heads, head_dim, dev.sms);
+}
+
+dspark_status dspark_attn_prompt(const dspark_heads *q, const dspark_heads *k, const dspark_heads *v, int64_t rows,
+                                 int64_t kv_rows, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                 int32_t dtype, const int32_t *row_off, const int32_t *kv_off, float scale,
+                                 int32_t causal, int64_t window, void *out, float *lse, void *workspace,
+                                 size_t workspace_bytes, int32_t *dev_status, void *stream) {
+  if (!q || !k || !v || !row_off || !kv_off || !out || !dev_status) return DSPARK_ERR_NULL;
+  if (dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_DTYPE;
+  dspark_status st = check_prompt(rows, kv_rows, B, q_heads, kv_heads, head_dim);
+  if (st == DSPARK_OK) st = check_heads(*q, dtype);
+  if (st == DSPARK_OK && kv_rows) st = check_heads(*k, dtype);
+  if (st == DSPARK_OK && kv_rows) st = check_heads(*v, dtype);
+  if (st != DSPARK_OK) return st;
+  if (!std::isfinite(scale) || !std::isfinite(scale * kLog2e) || window < 0 || window > kMaxRows) return DSPARK_ERR_DIMS;
+  for (const dspark_heads *t : {k, v})
+    if (kv_rows && !prompt_layout_ok(kv_rows, kv_heads, head_dim, t->row_stride, t->head_stride)) return DSPARK_ERR_UNSUPPORTED;
+  if (!aligned16(out)) return DSPARK_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return DSPARK_ERR_CUDA;
+  if (dev.major != 10 || dev.minor != 3) return DSPARK_ERR_UNSUPPORTED;
+  PromptArgs a = {};
+  a.q = q->data, a.q_row = q->row_stride, a.q_head = q->head_stride;
+  a.k = k->data, a.k_row = k->row_stride, a.k_head = k->head_stride;
+  a.v = v->data, a.v_row = v->row_stride, a.v_head = v->head_stride;
+  a.out = out, a.lse = lse;
+  a.row_off = row_off, a.kv_off = kv_off;
+  a.B = B, a.rows = rows, a.kv_rows = kv_rows;
+  a.Hq = q_heads, a.Hkv = kv_heads, a.D = head_dim, a.group = q_heads / kv_heads;
+  a.causal = causal != 0, a.window = (int)window, a.dtype = dtype;
+  a.scale_log2 = scale * kLog2e;
+  a.partial = (float *)workspace;
+  a.dev_status = dev_status;
+  const int64_t need = prompt_workspace_bytes(rows, kv_rows, B, q_heads, kv_heads, head_dim, dev.sms);
+  if (need && (!workspace || !aligned256(workspace) || workspace_bytes < (size_t)need)) return DSPARK_ERR_WORKSPACE;
+  return launch_prompt(a, (cudaStream_t)stream, dev.sms) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
 dspark_status dspark_logits_penalize(const void *logits, int32_t dtype, int64_t rows, int64_t V, int64_t B,
                                      const int32_t *row_off, const dspark_penalties *p, void *out,
                                      int32_t *dev_status, void *stream) {

@@ -73,6 +73,20 @@ struct AttendArgs {
   int32_t *dev_status;
 };
 
+struct PromptArgs {
+  const void *q, *k, *v;              // [rows, Hq, D], [kv_rows, Hkv, D], with strides in elements
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+  void *out;                          // contiguous [rows, Hq, D]
+  float *lse;                         // [rows, Hq] or null
+  const int32_t *row_off, *kv_off;
+  int64_t B, rows, kv_rows, units;
+  int Hq, Hkv, D, group, causal, window, dtype, parts;
+  int k_x, k_z, v_x, v_z;             // a head's place in the tensor copies' coordinates
+  float scale_log2;
+  float *partial;                     // workspace of the split form
+  int32_t *dev_status;
+};
+
 struct PenalizeArgs {
   const void *logits;
   void *out;                          // may be `logits`
@@ -90,6 +104,10 @@ cudaError_t launch_cache_read(const CacheReadArgs &a, cudaStream_t s);
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s, int sms);
 // Bytes of AttendArgs::partial that a call needs; len: tokens that its page table can name.
 int64_t attend_workspace_bytes(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int64_t rows, int sms);
+cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t s, int sms);
+int64_t prompt_workspace_bytes(int64_t rows, int64_t kv_rows, int64_t B, int Hq, int Hkv, int D, int sms);
+// Whether tensor copies can take keys or values of these strides.
+bool prompt_layout_ok(int64_t kv_rows, int Hkv, int D, int64_t row, int64_t head);
 cudaError_t launch_penalize(const PenalizeArgs &a, cudaStream_t s, int sms);
 
 // The status word as a kernel finds it, through the SM's first-level cache: a warp a row means thousands of

@@ -31,6 +31,8 @@ struct {
   decltype(&dspark_attn_paged_workspace_bytes) workspace_bytes;
   decltype(&dspark_attn_paged) paged;
   decltype(&dspark_logits_penalize) penalize;
+  decltype(&dspark_attn_prompt_workspace_bytes) prompt_workspace_bytes;
+  decltype(&dspark_attn_prompt) prompt;
 } api;
 
 struct Refused {};   // a Python error is set
@@ -159,6 +161,22 @@ struct Result {
       data = t.data_ptr();
       object = on.hand_out(std::move(t));
     }
+  }
+  // The given workspace where it is fit for `need` bytes, or a new one; returns its bytes.
+  int64_t workspace(PyObject *given, int64_t need, const Stream &on) {
+    if (!need) return 0;
+    if (given != Py_None) {
+      const at::Tensor &w = cuda_tensor(given, "workspace");
+      const bool fit = w.is_contiguous() && w.get_device() == on.device() && (uintptr_t)w.data_ptr() % 256 == 0;
+      if (fit && (int64_t)w.nbytes() >= need) {
+        data = w.data_ptr();
+        Py_INCREF(given);
+        object = given;
+        return (int64_t)w.nbytes();
+      }
+    }
+    make(Py_None, "workspace", at::kByte, {need}, on);
+    return need;
   }
   void status(PyObject *given, const Stream &on) {
     const int dev = on.device();
@@ -335,25 +353,56 @@ PyObject *paged(PyObject *const *v) {
   if (rows) {
     const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
     const int64_t need = (int64_t)api.workspace_bytes((int32_t)hq, cache, &where, max_rows);
-    int64_t have = 0;
-    if (need) {
-      if (v[12] != Py_None) {
-        const at::Tensor &w = cuda_tensor(v[12], "workspace");
-        have = w.is_contiguous() && w.get_device() == dev && (uintptr_t)w.data_ptr() % 256 == 0 ? (int64_t)w.nbytes() : 0;
-        if (have >= need) {
-          ws.data = w.data_ptr();
-          Py_INCREF(v[12]);
-          ws.object = v[12];
-        }
-      }
-      if (!ws.data) {
-        ws.make(Py_None, "workspace", at::kByte, {need}, on);
-        have = need;
-      }
-    }
+    const int64_t have = ws.workspace(v[12], need, on);
     const double scale = v[6] == Py_None ? 1.0 / std::sqrt((double)d) : real(v[6]);
     const int e = api.paged(&qh, (int32_t)hq, code, cache, &where, max_rows, (float)scale, PyObject_IsTrue(v[7]), window, o.data,
                             (float *)lse.data, ws.data, (size_t)have, (int32_t *)st.data, on.raw());
+    if (e) return PyLong_FromLong(e);
+  }
+  return answer({{"out", &o}, {"lse", &lse}, {"status", &st}, {"workspace", &ws}});
+}
+
+// q, k, v, row_off, kv_off, scale, causal, window, want_lse, out, workspace, status, stream
+PyObject *prompt(PyObject *const *v) {
+  const at::Tensor &q = cuda_tensor(v[0], "q"), &k = cuda_tensor(v[1], "k"), &off = cuda_tensor(v[3], "row_off");
+  const int dev = q.get_device(), code = dtype_code(q, "q", {at::kBFloat16, at::kHalf});
+  const Stream on(v[12], dev);
+  if (q.dim() != 3 || k.dim() != 3) refuse(PyExc_ValueError, "q and k must be [rows, heads, D]");
+  const at::ScalarType dt = q.scalar_type();
+  const int64_t rows = q.size(0), hq = q.size(1), d = q.size(2), kv_rows = k.size(0), hkv = k.size(1), window = whole(v[7]);
+  out_is_dict(v[9]);
+  if (d != 64 && d != 128) refuse(PyExc_ValueError, "heads must have 64 or 128 dimensions, got " + std::to_string(d));
+  if (!hkv || !hq || hq % hkv)
+    refuse(PyExc_ValueError, std::to_string(hq) + " query heads are no multiple of " + std::to_string(hkv) + " key/value heads");
+  if (window < 0) refuse(PyExc_ValueError, "window must not be negative");
+  if (off.dim() != 1 || !off.size(0)) refuse(PyExc_ValueError, "row_off must be [B + 1] int32");
+  const int64_t B = off.size(0) - 1;
+  const dspark_heads qh = heads(v[0], "q", dt, rows, hq, d, dev), kh = heads(v[1], "k", dt, kv_rows, hkv, d, dev),
+                     vh = heads(v[2], "v", dt, kv_rows, hkv, d, dev);
+  for (const dspark_heads *t : {&kh, &vh}) {
+    const std::string name = t == &kh ? "k" : "v";
+    const int64_t sr = t->row_stride, sh = t->head_stride;
+    if ((kv_rows > 1 && !sr) || (hkv > 1 && !sh)) refuse(PyExc_ValueError, name + " must not be broadcast along rows or heads");
+    if (kv_rows > 1 && hkv > 1 && (hkv - 1) * sh + d > sr && sh % sr)
+      refuse(PyExc_ValueError, name + " must have its heads inside its rows, or its rows inside its heads with the heads' stride "
+                                      "a multiple of the rows'");
+  }
+  const int32_t *row_off = like<int32_t>(v[3], "row_off", at::kInt, {B + 1}, dev);
+  const int32_t *kv_off = v[4] == Py_None ? row_off : like<int32_t>(v[4], "kv_off", at::kInt, {B + 1}, dev);
+  if (v[4] == Py_None && kv_rows != rows)
+    refuse(PyExc_ValueError, "k has " + std::to_string(kv_rows) + " rows and q " + std::to_string(rows) + ": give kv_off");
+  Result o, lse, ws, st;
+  o.make(v[9], "out", dt, {rows, hq, d}, on);
+  if (PyObject_IsTrue(v[8])) lse.make(v[9], "lse", at::kFloat, {rows, hq}, on);
+  st.status(v[11], on);
+  if (rows && B) {
+    const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
+    const int64_t have = ws.workspace(
+        v[10], (int64_t)api.prompt_workspace_bytes(rows, kv_rows, B, (int32_t)hq, (int32_t)hkv, (int32_t)d), on);
+    const double scale = v[5] == Py_None ? 1.0 / std::sqrt((double)d) : real(v[5]);
+    const int e = api.prompt(&qh, &kh, &vh, rows, kv_rows, B, (int32_t)hq, (int32_t)hkv, (int32_t)d, code, row_off, kv_off,
+                             (float)scale, PyObject_IsTrue(v[6]), window, o.data, (float *)lse.data, ws.data, (size_t)have,
+                             (int32_t *)st.data, on.raw());
     if (e) return PyLong_FromLong(e);
   }
   return answer({{"out", &o}, {"lse", &lse}, {"status", &st}, {"workspace", &ws}});
@@ -412,8 +461,9 @@ PyObject *init(PyObject *const *v) {
 }
 
 #define ENTRY(f, n) {#f, (PyCFunction)(void (*)(void))entry<f, n>, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(init, 6),   ENTRY(norm_rope, 10), ENTRY(append, 16),
-                         ENTRY(read, 9),   ENTRY(paged, 15),     ENTRY(penalize, 15), {}};
+PyMethodDef methods[] = {ENTRY(init, 8),   ENTRY(norm_rope, 10), ENTRY(append, 16),
+                         ENTRY(read, 9),   ENTRY(paged, 15),     ENTRY(penalize, 15),
+                         ENTRY(prompt, 13), {}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};
 
 }  // namespace

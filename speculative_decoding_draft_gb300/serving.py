@@ -57,12 +57,16 @@ def declare(L) -> None:
             ("dspark_attn_append", [H, H, H, i32, i32, C, W, P, R, P, P, f, P, P, P]),
             ("dspark_attn_cache_read", [C, W, P, P, P, P, P, P]),
             ("dspark_attn_paged", [H, i32, i32, C, W, i64, f, i32, i64, P, P, P, ctypes.c_size_t, P, P]),
-            ("dspark_logits_penalize", [P, i32, i64, i64, i64, P, ctypes.POINTER(_Penalties), P, P, P])):
+            ("dspark_logits_penalize", [P, i32, i64, i64, i64, P, ctypes.POINTER(_Penalties), P, P, P]),
+            ("dspark_attn_prompt", [H, H, H, i64, i64, i64, i32, i32, i32, i32, P, P, f, i32, i64, P, P, P,
+                                    ctypes.c_size_t, P, P])):
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
     L.dspark_attn_paged_workspace_bytes.argtypes = [i32, C, W, i64]
     L.dspark_attn_paged_workspace_bytes.restype = ctypes.c_size_t
+    L.dspark_attn_prompt_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32]
+    L.dspark_attn_prompt_workspace_bytes.restype = ctypes.c_size_t
 
 
 _binding = None
@@ -80,7 +84,8 @@ def _native():
                                         "`python -c 'import __graft_entry__ as g; g.build()'`") from None
         native.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "dspark_attn_norm_rope", "dspark_attn_append", "dspark_attn_cache_read",
-            "dspark_attn_paged_workspace_bytes", "dspark_attn_paged", "dspark_logits_penalize")))
+            "dspark_attn_paged_workspace_bytes", "dspark_attn_paged", "dspark_logits_penalize",
+            "dspark_attn_prompt_workspace_bytes", "dspark_attn_prompt")))
         _binding = native
     return _binding
 
@@ -261,6 +266,27 @@ def attend_paged(q, cache: PagedCache, row_off, kv_len, page_table, *, scale: Op
     _of(cache, PagedCache, "cache")
     return _done(_native().paged(q, cache._at, cache.device, row_off, kv_len, page_table, scale, causal, window, max_rows,
                                  want_lse, out, workspace, status, _raw(stream)), "dspark_attn_paged")
+
+
+# ---------------------------------------------------------------------------
+# whole prompts
+# ---------------------------------------------------------------------------
+def attend_prompt(q, k, v, row_off, *, kv_off=None, scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                  want_lse: bool = False, out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Attention of whole prompts over keys and values in 16 bits (C ABI dspark_attn_prompt).
+
+    q [rows, Hq, D], k, v [kv_rows, Hkv, D] bfloat16 or float16, D 64 or 128, Hq a multiple of Hkv (rows and heads may
+    be strided, as in a view of a fused projection or of [heads, rows, D], but k and v not broadcast); row_off [B+1]
+    int32: request r's queries.  kv_off [B+1] int32 (default: row_off): its keys and values, of which the queries are
+    the last where there are more (a later piece of a prompt over its earlier ones).  scale: 1/sqrt(D) unless given.
+    Row j of n sees its request's m tokens up to m - n + j (causal) or all, and with window > 0 only the last
+    ``window`` of them; a row that sees nothing gets 0 and lse -inf, and what masked tokens hold (infinities, NaN)
+    changes nothing.  Returns out [rows, Hq, D] and, with want_lse, lse [rows, Hq] float32.  Rows at and past row_off[B]
+    are left alone.
+    """
+    return _done(_native().prompt(q, k, v, row_off, kv_off, scale, causal, window, want_lse, out, workspace, status,
+                                  _raw(stream)), "dspark_attn_prompt")
 
 
 # ---------------------------------------------------------------------------
