@@ -533,6 +533,33 @@ dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t 
                                 int64_t window, void *out, float *lse, void *workspace, size_t workspace_bytes,
                                 int32_t *dev_status, void *stream);
 
+/* A paged key/value cache in 8 bits: data [pages][kv_heads][keys, values][page_size][head_dim] e4m3 elements and
+ * scales [pages][kv_heads][keys, values][page_size / 16] bytes e + 127, the scale 2^e, e in -32 .. 31, of a block of 16
+ * tokens of one head.  A token's elements lie in pieces of 16: piece c at place c ^ (t % 8) of token t of its page
+ * where head_dim is 128, at c ^ (t / 2 % 4) where it is 64.  head_dim 64 or 128; page_size a multiple of 16 to 4096;
+ * data 16-byte aligned. */
+typedef struct {
+  void *data, *scales;
+  int64_t pages;
+  int32_t kv_heads, head_dim, page_size;
+} dspark_byte_cache;
+
+/* As dspark_attn_append, to a cache in 8 bits: e = the smallest with 448 2^e at or above every finite magnitude that
+ * has been written to the block since a call began it at its first token (e stays in its range), element = e4m3(y 2^-e)
+ * to nearest, ties to even; infinities and what passes the range become the largest element, a NaN stays one.  Where
+ * a call goes on in a block and e rises, the elements that are there are rounded again on the new scale.  Rows may take
+ * the places of earlier ones (drafted tokens that were rejected); the scale keeps what those needed.  A block that
+ * a call writes to belongs to one request. */
+dspark_status dspark_attn_append_byte(const dspark_heads *k, const dspark_heads *v, const dspark_heads *q, int32_t q_heads,
+                                      int32_t dtype, const dspark_byte_cache *cache, const dspark_ragged *where,
+                                      const int32_t *positions, const dspark_rope *rope, const void *q_weight,
+                                      const void *k_weight, float eps, void *q_out, int32_t *dev_status, void *stream);
+
+/* What a cache in 8 bits holds of the rows' tokens, as values: k and v [rows, kv_heads, D] of dtype F32 and BF16 (exact)
+ * or F16 (rounded, infinite past its range). */
+dspark_status dspark_attn_cache_read_byte(const dspark_byte_cache *cache, const dspark_ragged *where, int32_t dtype,
+                                          void *k, void *v, int32_t *dev_status, void *stream);
+
 /* Attention of whole prompts: ragged rows over ragged keys and values in 16 bits.  Request r's queries are rows
  * row_off[r] .. row_off[r+1]-1 of q [rows, q_heads, D] and its m_r tokens are rows kv_off[r] .. kv_off[r+1]-1 of k and
  * v [kv_rows, kv_heads, D] (kv_off may be row_off; more tokens than queries: earlier pieces of the same prompt come

@@ -56,7 +56,7 @@ EXPORTED_SYMBOLS = [
     "dspark_verify_ragged", "dspark_verify_markov_workspace_bytes", "dspark_verify_markov",
     "dspark_attn_norm_rope", "dspark_attn_append", "dspark_attn_cache_read",
     "dspark_attn_paged_workspace_bytes", "dspark_attn_paged", "dspark_attn_prompt_workspace_bytes",
-    "dspark_attn_prompt",
+    "dspark_attn_prompt", "dspark_attn_append_byte", "dspark_attn_cache_read_byte",
     "dspark_logits_penalize", "dspark_status_string", "dspark_check", "dspark_version",
 ]
 
@@ -585,5 +585,5 @@ def verify_markov(U, E, W, anchor, draft_lse, draft_tok_logit, tgt_logits, tgt_o
 
 
 from . import serving  # noqa: E402
-from .serving import (PagedCache, Rope, attend_paged, attend_prompt, cache_append, cache_read, norm_rope,  # noqa: E402
-                      penalize_logits)
+from .serving import (PagedCache, PagedCache8, Rope, attend_paged, attend_prompt, cache_append, cache_read,  # noqa: E402
+                      norm_rope, penalize_logits)

@@ -609,6 +609,14 @@ dspark_status check_cache(const dspark_cache *c) {
   return aligned16(c->data) ? DSPARK_OK : DSPARK_ERR_UNSUPPORTED;
 }
 
+dspark_status check_byte_cache(const dspark_byte_cache *c) {
+  if (!c || !c->data || !c->scales) return DSPARK_ERR_NULL;
+  if (c->pages < 1 || c->pages > ((int64_t)1 << 40) || c->kv_heads < 1 || c->kv_heads > kMaxHeads) return DSPARK_ERR_DIMS;
+  if (c->page_size < 16 || c->page_size % 16 || c->page_size > 4096) return DSPARK_ERR_DIMS;
+  if (c->head_dim != 64 && c->head_dim != 128) return DSPARK_ERR_UNSUPPORTED;
+  return aligned16(c->data) ? DSPARK_OK : DSPARK_ERR_UNSUPPORTED;
+}
+
 dspark_status check_ragged(const dspark_ragged *t, int page_size) {
   if (!t || !t->row_off || !t->kv_len || !t->page_table) return DSPARK_ERR_NULL;
   // token positions are 32-bit inside the kernels
@@ -763,6 +771,66 @@ dspark_status dspark_attn_paged(const dspark_heads *q, int32_t q_heads, int32_t 
   const int64_t need = attend_workspace_bytes(a.B, a.Hkv, a.group, a.D, a.max_pages * a.page_size, a.max_rows, a.rows, dev.sms);
   if (need && (!workspace || !aligned256(workspace) || workspace_bytes < (size_t)need)) return DSPARK_ERR_WORKSPACE;
   return launch_attend(a, (cudaStream_t)stream, dev.sms) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+dspark_status dspark_attn_append_byte(const dspark_heads *k, const dspark_heads *v, const dspark_heads *q, int32_t q_heads,
+                                      int32_t dtype, const dspark_byte_cache *cache, const dspark_ragged *where,
+                                      const int32_t *positions, const dspark_rope *rope, const void *q_weight,
+                                      const void *k_weight, float eps, void *q_out, int32_t *dev_status, void *stream) {
+  if (!k || !v || !dev_status || (q != nullptr) != (q_out != nullptr)) return DSPARK_ERR_NULL;
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_DTYPE;
+  dspark_status st = check_byte_cache(cache);
+  if (st == DSPARK_OK) st = check_ragged(where, cache->page_size);
+  if (st == DSPARK_OK) st = check_heads(*k, dtype);
+  if (st == DSPARK_OK) st = check_heads(*v, dtype);
+  if (st == DSPARK_OK && q) st = check_heads(*q, dtype);
+  if (st == DSPARK_OK) st = check_weights(q_weight, k_weight);
+  if (st == DSPARK_OK) st = check_rope(rope, cache->head_dim);
+  if (st != DSPARK_OK) return st;
+  if ((q && (q_heads < 1 || q_heads > kMaxHeads)) || !(eps >= 0.0f)) return DSPARK_ERR_DIMS;
+  if (!aligned16(q_out)) return DSPARK_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return DSPARK_ERR_CUDA;
+  if (dev.major != 10 || dev.minor != 3) return DSPARK_ERR_UNSUPPORTED;
+  ByteHeadsArgs a = {};
+  if (q) a.q = q->data, a.q_row = q->row_stride, a.q_head = q->head_stride;
+  a.k = k->data, a.k_row = k->row_stride, a.k_head = k->head_stride;
+  a.v = v->data, a.v_row = v->row_stride, a.v_head = v->head_stride;
+  a.q_out = q_out;
+  a.q_weight = q ? q_weight : nullptr, a.k_weight = k_weight;
+  a.positions = positions;
+  if (rope) {
+    a.turns = (const unsigned long long *)rope->turns;
+    a.rot = rope->rotary_dim, a.interleaved = rope->interleaved != 0, a.gain = rope->gain;
+  }
+  a.rows = where->rows, a.Hq = q ? q_heads : 0, a.Hkv = cache->kv_heads, a.D = cache->head_dim, a.dtype = dtype;
+  a.eps = eps;
+  a.data = (uint8_t *)cache->data, a.scales = (uint8_t *)cache->scales, a.pages = cache->pages, a.page_size = cache->page_size;
+  a.B = where->B, a.max_pages = where->max_pages;
+  a.row_off = where->row_off, a.kv_len = where->kv_len, a.table = where->page_table;
+  a.dev_status = dev_status;
+  return launch_byte_append(a, (cudaStream_t)stream, dev.sms) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+dspark_status dspark_attn_cache_read_byte(const dspark_byte_cache *cache, const dspark_ragged *where, int32_t dtype,
+                                          void *k, void *v, int32_t *dev_status, void *stream) {
+  if (!k || !v || !dev_status) return DSPARK_ERR_NULL;
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_DTYPE;
+  dspark_status st = check_byte_cache(cache);
+  if (st == DSPARK_OK) st = check_ragged(where, cache->page_size);
+  if (st != DSPARK_OK) return st;
+  if (!aligned16(k) || !aligned16(v)) return DSPARK_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return DSPARK_ERR_CUDA;
+  if (dev.major != 10 || dev.minor != 3) return DSPARK_ERR_UNSUPPORTED;
+  ByteReadArgs a = {};
+  a.data = (const uint8_t *)cache->data, a.scales = (const uint8_t *)cache->scales, a.pages = cache->pages;
+  a.page_size = cache->page_size, a.Hkv = cache->kv_heads, a.D = cache->head_dim, a.dtype = dtype;
+  a.B = where->B, a.rows = where->rows, a.max_pages = where->max_pages;
+  a.row_off = where->row_off, a.kv_len = where->kv_len, a.table = where->page_table;
+  a.k = k, a.v = v;
+  a.dev_status = dev_status;
+  return launch_byte_read(a, (cudaStream_t)stream, dev.sms) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 static dspark_status check_prompt(int64_t rows, int64_t kv_rows, int64_t B, int32_t q_heads, int32_t kv_heads,

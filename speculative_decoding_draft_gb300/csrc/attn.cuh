@@ -59,6 +59,32 @@ struct CacheReadArgs {
   int32_t *dev_status;
 };
 
+// The cache in 8 bits: e4m3 elements [pages][Hkv][keys, values][page_size][D] and a power of two for 16 tokens of a
+// head, exponents + 127 [pages][Hkv][2][page_size / 16].
+struct ByteHeadsArgs {
+  const void *q, *k, *v;              // [rows, heads, D] with strides in elements
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+  void *q_out;                        // contiguous [rows, Hq, D]
+  const void *q_weight, *k_weight;    // [D] or null
+  const int32_t *positions;           // [rows] or null: the rows' places in the cache
+  const unsigned long long *turns;    // [rot / 2] or null: no rotation
+  int64_t rows, pages, max_pages, B;
+  int Hq, Hkv, D, rot, interleaved, dtype, page_size;
+  float gain, eps;
+  uint8_t *data, *scales;
+  const int32_t *row_off, *kv_len, *table;
+  int32_t *dev_status;
+};
+
+struct ByteReadArgs {
+  const uint8_t *data, *scales;
+  int64_t pages, max_pages, B, rows;
+  int Hkv, D, page_size, dtype;
+  const int32_t *row_off, *kv_len, *table;
+  void *k, *v;                        // contiguous [rows, Hkv, D]
+  int32_t *dev_status;
+};
+
 struct AttendArgs {
   const void *q;                      // [rows, Hq, D] with strides in elements
   int64_t q_row, q_head;
@@ -104,6 +130,8 @@ cudaError_t launch_cache_read(const CacheReadArgs &a, cudaStream_t s);
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s, int sms);
 // Bytes of AttendArgs::partial that a call needs; len: tokens that its page table can name.
 int64_t attend_workspace_bytes(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int64_t rows, int sms);
+cudaError_t launch_byte_append(const ByteHeadsArgs &a, cudaStream_t s, int sms);
+cudaError_t launch_byte_read(const ByteReadArgs &a, cudaStream_t s, int sms);
 cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t s, int sms);
 int64_t prompt_workspace_bytes(int64_t rows, int64_t kv_rows, int64_t B, int Hq, int Hkv, int D, int sms);
 // Whether tensor copies can take keys or values of these strides.

@@ -33,6 +33,8 @@ struct {
   decltype(&dspark_logits_penalize) penalize;
   decltype(&dspark_attn_prompt_workspace_bytes) prompt_workspace_bytes;
   decltype(&dspark_attn_prompt) prompt;
+  decltype(&dspark_attn_append_byte) append_byte;
+  decltype(&dspark_attn_cache_read_byte) read_byte;
 } api;
 
 struct Refused {};   // a Python error is set
@@ -274,8 +276,9 @@ PyObject *norm_rope(PyObject *const *v) {
 }
 
 // cache, device, k, v, row_off, kv_len, page_table, positions, rope, k_weight, q, q_weight, eps, out, status, stream
-PyObject *append(PyObject *const *v) {
-  const auto *cache = (const dspark_cache *)address(v[0]);
+template <class Cache, class Call>
+PyObject *append_to(PyObject *const *v, Call call) {
+  const auto *cache = (const Cache *)address(v[0]);
   const int dev = (int)whole(v[1]);
   const Stream on(v[15], dev);
   const at::Tensor &k = cuda_tensor(v[2], "k");
@@ -300,12 +303,15 @@ PyObject *append(PyObject *const *v) {
   st.status(v[14], on);
   if (rows) {
     const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
-    const int e = api.append(&kh, &vh, qo.data ? &qh : nullptr, (int32_t)hq, code, cache, &where, pos, rope, wq, wk,
+    const int e = call(&kh, &vh, qo.data ? &qh : nullptr, (int32_t)hq, code, cache, &where, pos, rope, wq, wk,
                              (float)real(v[12]), qo.data, (int32_t *)st.data, on.raw());
     if (e) return PyLong_FromLong(e);
   }
   return answer({{"q", &qo}, {"status", &st}});
 }
+
+PyObject *append(PyObject *const *v) { return append_to<dspark_cache>(v, api.append); }
+PyObject *append_byte(PyObject *const *v) { return append_to<dspark_byte_cache>(v, api.append_byte); }
 
 // cache, device, row_off, kv_len, page_table, rows, out, status, stream
 PyObject *read(PyObject *const *v) {
@@ -328,6 +334,28 @@ PyObject *read(PyObject *const *v) {
     if (e) return PyLong_FromLong(e);
   }
   return answer({{"k", &k}, {"k_scale", &ks}, {"v", &vo}, {"v_scale", &vs}, {"status", &st}});
+}
+
+// cache, device, row_off, kv_len, page_table, rows, dtype (a dspark_dtype), out, status, stream
+PyObject *read_byte(PyObject *const *v) {
+  const auto *cache = (const dspark_byte_cache *)address(v[0]);
+  const int dev = (int)whole(v[1]), code = (int)whole(v[6]);
+  const Stream on(v[9], dev);
+  const int64_t rows = whole(v[5]), d = cache->head_dim, h = cache->kv_heads;
+  if (rows < 0) refuse(PyExc_ValueError, "rows must not be negative");
+  out_is_dict(v[7]);
+  const dspark_ragged where = ragged(v[2], v[3], v[4], rows, dev);
+  const at::ScalarType dt = code == DSPARK_F32 ? at::kFloat : (code == DSPARK_BF16 ? at::kBFloat16 : at::kHalf);
+  Result k, vo, st;
+  k.make(v[7], "k", dt, {rows, h, d}, on);
+  vo.make(v[7], "v", dt, {rows, h, d}, on);
+  st.status(v[8], on);
+  if (rows) {
+    const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
+    const int e = api.read_byte(cache, &where, code, k.data, vo.data, (int32_t *)st.data, on.raw());
+    if (e) return PyLong_FromLong(e);
+  }
+  return answer({{"k", &k}, {"v", &vo}, {"status", &st}});
 }
 
 // q, cache, device, row_off, kv_len, page_table, scale, causal, window, max_rows, want_lse, out, workspace, status, stream
@@ -461,9 +489,9 @@ PyObject *init(PyObject *const *v) {
 }
 
 #define ENTRY(f, n) {#f, (PyCFunction)(void (*)(void))entry<f, n>, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(init, 8),   ENTRY(norm_rope, 10), ENTRY(append, 16),
+PyMethodDef methods[] = {ENTRY(init, 10),   ENTRY(norm_rope, 10), ENTRY(append, 16),
                          ENTRY(read, 9),   ENTRY(paged, 15),     ENTRY(penalize, 15),
-                         ENTRY(prompt, 13), {}};
+                         ENTRY(prompt, 13), ENTRY(append_byte, 16), ENTRY(read_byte, 10), {}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};
 
 }  // namespace

@@ -35,6 +35,11 @@ class _Cache(ctypes.Structure):
                 ("v_scale", ctypes.c_float)]
 
 
+class _ByteCache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
 class _Ragged(ctypes.Structure):
     _fields_ = [("row_off", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
                 ("B", ctypes.c_int64), ("rows", ctypes.c_int64), ("max_pages", ctypes.c_int64)]
@@ -51,7 +56,7 @@ class _Penalties(ctypes.Structure):
 def declare(L) -> None:
     """Argument types of the library's entry points (called by ``lib()``)."""
     P, i64, i32, f = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
-    H, R, C, W = (ctypes.POINTER(t) for t in (_Heads, _Rope, _Cache, _Ragged))
+    H, R, C, W, C8 = (ctypes.POINTER(t) for t in (_Heads, _Rope, _Cache, _Ragged, _ByteCache))
     for name, args in (
             ("dspark_attn_norm_rope", [H, H, i64, i32, i32, i32, i32, P, R, P, P, f, P, P, P, P]),
             ("dspark_attn_append", [H, H, H, i32, i32, C, W, P, R, P, P, f, P, P, P]),
@@ -59,7 +64,9 @@ def declare(L) -> None:
             ("dspark_attn_paged", [H, i32, i32, C, W, i64, f, i32, i64, P, P, P, ctypes.c_size_t, P, P]),
             ("dspark_logits_penalize", [P, i32, i64, i64, i64, P, ctypes.POINTER(_Penalties), P, P, P]),
             ("dspark_attn_prompt", [H, H, H, i64, i64, i64, i32, i32, i32, i32, P, P, f, i32, i64, P, P, P,
-                                    ctypes.c_size_t, P, P])):
+                                    ctypes.c_size_t, P, P]),
+            ("dspark_attn_append_byte", [H, H, H, i32, i32, C8, W, P, R, P, P, f, P, P, P]),
+            ("dspark_attn_cache_read_byte", [C8, W, i32, P, P, P, P])):
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
@@ -85,7 +92,8 @@ def _native():
         native.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "dspark_attn_norm_rope", "dspark_attn_append", "dspark_attn_cache_read",
             "dspark_attn_paged_workspace_bytes", "dspark_attn_paged", "dspark_logits_penalize",
-            "dspark_attn_prompt_workspace_bytes", "dspark_attn_prompt")))
+            "dspark_attn_prompt_workspace_bytes", "dspark_attn_prompt", "dspark_attn_append_byte",
+            "dspark_attn_cache_read_byte")))
         _binding = native
     return _binding
 
@@ -180,7 +188,8 @@ def norm_rope(q, k=None, positions=None, rope: Optional[Rope] = None, *, q_weigh
 
 def _of(x, kind, name):
     if not isinstance(x, kind):
-        raise TypeError(f"{name} must be a {kind.__name__}")
+        kinds = kind if isinstance(kind, tuple) else (kind,)
+        raise TypeError(f"{name} must be a {' or a '.join(k.__name__ for k in kinds)}")
     return x
 
 
@@ -223,29 +232,82 @@ class PagedCache:
                    page_size, k_scale=k_scale, v_scale=v_scale)
 
 
-def cache_append(cache: PagedCache, k, v, row_off, kv_len, page_table, *, positions=None, rope: Optional[Rope] = None,
+class PagedCache8:
+    """A paged key/value cache in 8 bits: data uint8 [pages, kv_heads, 2, page_size, D] (keys, then values; e4m3
+    elements) and scales uint8 [pages, kv_heads, 2, page_size/16], a power of two for a block of 16 tokens of a head
+    (see include/dspark.h for the places of a token's elements).  No range has to be chosen: a block's scale follows
+    its loudest token."""
+
+    def __init__(self, data: torch.Tensor, scales: torch.Tensor):
+        for name, x in (("data", data), ("scales", scales)):
+            if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.uint8:
+                raise TypeError(f"{name} must be a uint8 CUDA tensor")
+        if data.dim() != 5 or data.shape[2] != 2 or not data.is_contiguous() or data.data_ptr() % 16:
+            raise ValueError("data must be contiguous [pages, kv_heads, 2, page_size, D], 16-byte aligned")
+        pages, heads, _, page_size, dim = data.shape
+        if page_size < 16 or page_size % 16 or page_size > 4096:
+            raise ValueError(f"page_size must be a multiple of 16 to 4096, got {page_size}")
+        if dim not in (64, 128):
+            raise ValueError("the cache holds heads of 64 or 128 dimensions")
+        if scales.shape != (pages, heads, 2, page_size // 16) or not scales.is_contiguous() or scales.device != data.device:
+            raise ValueError(f"scales must be contiguous {(pages, heads, 2, page_size // 16)} on {data.device}")
+        self.data, self.scales, self.page_size = data, scales, page_size
+        self.pages, self.kv_heads, self.head_dim = pages, heads, dim
+        self.device = data.get_device()
+        self._c = _ByteCache(data.data_ptr(), scales.data_ptr(), pages, heads, dim, page_size)
+        self._at = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, head_dim: int, page_size: int = 64, *, device="cuda") -> "PagedCache8":
+        """A cache of zeros."""
+        if page_size < 16 or page_size % 16 or page_size > 4096:
+            raise ValueError(f"page_size must be a multiple of 16 to 4096, got {page_size}")
+        return cls(torch.zeros(pages, kv_heads, 2, page_size, head_dim, dtype=torch.uint8, device=device),
+                   torch.zeros(pages, kv_heads, 2, page_size // 16, dtype=torch.uint8, device=device))
+
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def cache_append(cache, k, v, row_off, kv_len, page_table, *, positions=None, rope: Optional[Rope] = None,
                  k_weight=None, q=None, q_weight=None, eps: float = 1e-6, out: Optional[dict] = None,
                  status: Optional[torch.Tensor] = None, stream=None) -> dict:
-    """Append the rows' keys and values to the cache, keys normed and rotated on the way (C ABI dspark_attn_append).
+    """Append the rows' keys and values to the cache, keys normed and rotated on the way (C ABI dspark_attn_append;
+    to a PagedCache8 dspark_attn_append_byte).
 
     k, v [rows, Hkv, D]; row_off [B+1], kv_len [B] (with these rows among them), page_table [B, max_pages], all
     int32; positions [rows] int32 or None (a row's place in its request); with q [rows, Hq, D] the queries are
-    normed and rotated in the same pass and returned as q (contiguous).  Two rows must not name the same place.
+    normed and rotated in the same pass and returned as q (contiguous).  Two rows must not name the same place, and in
+    a PagedCache8 a block of 16 tokens that is written to belongs to one request.
     """
-    _of(cache, PagedCache, "cache")
+    _of(cache, (PagedCache, PagedCache8), "cache")
     turn = None if rope is None else _of(rope, Rope, "rope")._at
     if turn is not None and rope.device != cache.device:
         raise ValueError(f"rope must be on {cache.data.device}, got {rope.turns.device}")
+    if isinstance(cache, PagedCache8):
+        return _done(_native().append_byte(cache._at, cache.device, k, v, row_off, kv_len, page_table, positions, turn,
+                                           k_weight, q, q_weight, eps, out, status, _raw(stream)), "dspark_attn_append_byte")
     return _done(_native().append(cache._at, cache.device, k, v, row_off, kv_len, page_table, positions, turn, k_weight, q,
                                   q_weight, eps, out, status, _raw(stream)), "dspark_attn_append")
 
 
-def cache_read(cache: PagedCache, row_off, kv_len, page_table, rows: int, *, out: Optional[dict] = None,
-               status: Optional[torch.Tensor] = None, stream=None) -> dict:
+def cache_read(cache, row_off, kv_len, page_table, rows: int, *, dtype: Optional[torch.dtype] = None,
+               out: Optional[dict] = None, status: Optional[torch.Tensor] = None, stream=None) -> dict:
     """What the cache holds of the rows' tokens (C ABI dspark_attn_cache_read): k, v [rows, Hkv, D] and k_scale,
     v_scale [rows, Hkv, D/16], float8_e4m3fn and exact; an element's value is element * scale * the cache's scale.
-    A request's whole text: row_off over kv_len rows each."""
-    _of(cache, PagedCache, "cache")
+    A request's whole text: row_off over kv_len rows each.
+
+    Of a PagedCache8 the values themselves (C ABI dspark_attn_cache_read_byte): k, v [rows, Hkv, D] of ``dtype``
+    (bfloat16 unless given, or float32: exact; float16: rounded), as attend_prompt takes them."""
+    _of(cache, (PagedCache, PagedCache8), "cache")
+    if isinstance(cache, PagedCache8):
+        code = _DTYPES.get(torch.bfloat16 if dtype is None else dtype)
+        if code is None:
+            raise TypeError(f"dtype must be torch.bfloat16, torch.float32 or torch.float16, got {dtype}")
+        return _done(_native().read_byte(cache._at, cache.device, row_off, kv_len, page_table, rows, code, out, status,
+                                         _raw(stream)), "dspark_attn_cache_read_byte")
+    if dtype is not None:
+        raise TypeError("a cache in 4 bits is read as elements and scales: no dtype")
     return _done(_native().read(cache._at, cache.device, row_off, kv_len, page_table, rows, out, status, _raw(stream)),
                  "dspark_attn_cache_read")
 
