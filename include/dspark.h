@@ -560,6 +560,16 @@ dspark_status dspark_attn_append_byte(const dspark_heads *k, const dspark_heads 
 dspark_status dspark_attn_cache_read_byte(const dspark_byte_cache *cache, const dspark_ragged *where, int32_t dtype,
                                           void *k, void *v, int32_t *dev_status, void *stream);
 
+/* As dspark_attn_paged, over a cache in 8 bits.  The workspace is always needed; its contents do not matter, and two
+ * calls that may run at the same time need two. */
+size_t dspark_attn_paged_byte_workspace_bytes(int32_t q_heads, const dspark_byte_cache *cache, const dspark_ragged *where,
+                                              int64_t max_rows);
+
+dspark_status dspark_attn_paged_byte(const dspark_heads *q, int32_t q_heads, int32_t dtype, const dspark_byte_cache *cache,
+                                     const dspark_ragged *where, int64_t max_rows, float scale, int32_t causal,
+                                     int64_t window, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                     int32_t *dev_status, void *stream);
+
 /* Attention of whole prompts: ragged rows over ragged keys and values in 16 bits.  Request r's queries are rows
  * row_off[r] .. row_off[r+1]-1 of q [rows, q_heads, D] and its m_r tokens are rows kv_off[r] .. kv_off[r+1]-1 of k and
  * v [kv_rows, kv_heads, D] (kv_off may be row_off; more tokens than queries: earlier pieces of the same prompt come

@@ -57,6 +57,7 @@ EXPORTED_SYMBOLS = [
     "dspark_attn_norm_rope", "dspark_attn_append", "dspark_attn_cache_read",
     "dspark_attn_paged_workspace_bytes", "dspark_attn_paged", "dspark_attn_prompt_workspace_bytes",
     "dspark_attn_prompt", "dspark_attn_append_byte", "dspark_attn_cache_read_byte",
+    "dspark_attn_paged_byte_workspace_bytes", "dspark_attn_paged_byte",
     "dspark_logits_penalize", "dspark_status_string", "dspark_check", "dspark_version",
 ]
 

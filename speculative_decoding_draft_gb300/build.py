@@ -24,7 +24,8 @@ LIB = os.path.join(HERE, "libdspark.so")
 BUILD_BOUNDS = os.path.join(HERE, "_build_bounds")
 LIB_BOUNDS = os.path.join(HERE, "libdspark_bounds.so")
 SOURCES = ["api.cu", "schedule.cu", "schedule_noalloc.cu", "verify.cu", "draft_simt.cu", "draft_tc.cu", "rope_cache.cu",
-           "attend.cu", "penalize.cu", "prompt.cu", "byte_cache.cu"]
+           "attend.cu", "penalize.cu", "prompt.cu", "byte_cache.cu",
+           "byte_attend.cu"]
 BINDING = os.path.join(HERE, "_binding.so")   # the native binding of the serving operators (host code only)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

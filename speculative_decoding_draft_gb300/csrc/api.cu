@@ -833,6 +833,55 @@ dspark_status dspark_attn_cache_read_byte(const dspark_byte_cache *cache, const 
   return launch_byte_read(a, (cudaStream_t)stream, dev.sms) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
+static dspark_status check_byte_attend(int32_t q_heads, const dspark_byte_cache *cache, const dspark_ragged *where,
+                                       int64_t max_rows) {
+  dspark_status st = check_byte_cache(cache);
+  if (st == DSPARK_OK) st = check_ragged(where, cache->page_size);
+  if (st != DSPARK_OK) return st;
+  // a request's row-heads are 32-bit inside the kernel
+  if (q_heads < 1 || q_heads > kMaxHeads || q_heads % cache->kv_heads || max_rows < 1 || max_rows > (1 << 20)) return DSPARK_ERR_DIMS;
+  return DSPARK_OK;
+}
+
+size_t dspark_attn_paged_byte_workspace_bytes(int32_t q_heads, const dspark_byte_cache *cache, const dspark_ragged *where,
+                                              int64_t max_rows) {
+  DeviceInfo dev;
+  if (check_byte_attend(q_heads, cache, where, max_rows) != DSPARK_OK || !device_info(&dev)) return 0;
+  return (size_t)byte_attend_workspace_bytes(q_heads / cache->kv_heads, cache->head_dim,
+                                             max_rows < where->rows ? max_rows : where->rows, dev.sms);
+}
+
+dspark_status dspark_attn_paged_byte(const dspark_heads *q, int32_t q_heads, int32_t dtype, const dspark_byte_cache *cache,
+                                     const dspark_ragged *where, int64_t max_rows, float scale, int32_t causal,
+                                     int64_t window, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                     int32_t *dev_status, void *stream) {
+  if (!q || !out || !dev_status) return DSPARK_ERR_NULL;
+  if (dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_DTYPE;
+  dspark_status st = check_byte_attend(q_heads, cache, where, max_rows);
+  if (st == DSPARK_OK) st = check_heads(*q, dtype);
+  if (st != DSPARK_OK) return st;
+  if (!std::isfinite(scale) || !std::isfinite(scale * kLog2e) || window < 0 || window > kMaxRows) return DSPARK_ERR_DIMS;
+  if (!aligned16(out)) return DSPARK_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return DSPARK_ERR_CUDA;
+  if (dev.major != 10 || dev.minor != 3) return DSPARK_ERR_UNSUPPORTED;
+  ByteAttendArgs a = {};
+  a.q = q->data, a.q_row = q->row_stride, a.q_head = q->head_stride;
+  a.out = out, a.lse = lse;
+  a.data = (const uint8_t *)cache->data, a.scales = (const uint8_t *)cache->scales, a.pages = cache->pages;
+  a.page_size = cache->page_size, a.Hq = q_heads, a.Hkv = cache->kv_heads, a.D = cache->head_dim;
+  a.group = q_heads / cache->kv_heads;
+  a.B = where->B, a.rows = where->rows, a.max_pages = where->max_pages;
+  a.row_off = where->row_off, a.kv_len = where->kv_len, a.table = where->page_table;
+  a.causal = causal != 0, a.window = (int)window, a.max_rows = (int)(max_rows < where->rows ? max_rows : where->rows);
+  a.dtype = dtype;
+  a.scale_log2 = scale * kLog2e;
+  a.dev_status = dev_status;
+  const int64_t need = byte_attend_workspace_bytes(a.group, a.D, a.max_rows, dev.sms);
+  if (!workspace || !aligned256(workspace) || workspace_bytes < (size_t)need) return DSPARK_ERR_WORKSPACE;
+  return launch_byte_attend(a, workspace, (cudaStream_t)stream, dev.sms) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
 static dspark_status check_prompt(int64_t rows, int64_t kv_rows, int64_t B, int32_t q_heads, int32_t kv_heads,
                                   int32_t head_dim) {
   if (rows < 1 || rows > kMaxRows || kv_rows < 0 || kv_rows > kMaxRows - 128 || B < 1 || B > kMaxB || q_heads < 1 ||

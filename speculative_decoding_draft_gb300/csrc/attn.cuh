@@ -99,6 +99,21 @@ struct AttendArgs {
   int32_t *dev_status;
 };
 
+struct ByteAttendArgs {
+  const void *q;                      // [rows, Hq, D] with strides in elements
+  int64_t q_row, q_head;
+  void *out;                          // contiguous [rows, Hq, D]
+  float *lse;                         // [rows, Hq] or null
+  const uint8_t *data, *scales;
+  int64_t pages, max_pages, B, rows;
+  int Hq, Hkv, D, page_size, group, causal, window, max_rows, dtype;
+  float scale_log2;
+  float *partial;                     // the workspace: pieces' sums, and which units they belong to
+  int4 *headers;
+  const int32_t *row_off, *kv_len, *table;
+  int32_t *dev_status;
+};
+
 struct PromptArgs {
   const void *q, *k, *v;              // [rows, Hq, D], [kv_rows, Hkv, D], with strides in elements
   int64_t q_row, q_head, k_row, k_head, v_row, v_head;
@@ -132,6 +147,8 @@ cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s, int sms);
 int64_t attend_workspace_bytes(int64_t B, int Hkv, int group, int D, int64_t len, int64_t max_rows, int64_t rows, int sms);
 cudaError_t launch_byte_append(const ByteHeadsArgs &a, cudaStream_t s, int sms);
 cudaError_t launch_byte_read(const ByteReadArgs &a, cudaStream_t s, int sms);
+cudaError_t launch_byte_attend(const ByteAttendArgs &a, void *workspace, cudaStream_t s, int sms);
+int64_t byte_attend_workspace_bytes(int group, int D, int64_t max_rows, int sms);
 cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t s, int sms);
 int64_t prompt_workspace_bytes(int64_t rows, int64_t kv_rows, int64_t B, int Hq, int Hkv, int D, int sms);
 // Whether tensor copies can take keys or values of these strides.

@@ -35,6 +35,8 @@ struct {
   decltype(&dspark_attn_prompt) prompt;
   decltype(&dspark_attn_append_byte) append_byte;
   decltype(&dspark_attn_cache_read_byte) read_byte;
+  decltype(&dspark_attn_paged_byte_workspace_bytes) paged_byte_workspace_bytes;
+  decltype(&dspark_attn_paged_byte) paged_byte;
 } api;
 
 struct Refused {};   // a Python error is set
@@ -359,9 +361,10 @@ PyObject *read_byte(PyObject *const *v) {
 }
 
 // q, cache, device, row_off, kv_len, page_table, scale, causal, window, max_rows, want_lse, out, workspace, status, stream
-PyObject *paged(PyObject *const *v) {
+template <class Cache, class Bytes, class Call>
+PyObject *paged_over(PyObject *const *v, Bytes bytes, Call call) {
   const at::Tensor &q = cuda_tensor(v[0], "q");
-  const auto *cache = (const dspark_cache *)address(v[1]);
+  const auto *cache = (const Cache *)address(v[1]);
   const int dev = (int)whole(v[2]), code = dtype_code(q, "q", {at::kBFloat16, at::kHalf});
   const Stream on(v[14], dev);
   if (q.dim() != 3) refuse(PyExc_ValueError, "q must be [rows, heads, D]");
@@ -380,14 +383,19 @@ PyObject *paged(PyObject *const *v) {
   st.status(v[13], on);
   if (rows) {
     const c10::cuda::CUDAGuard here((c10::DeviceIndex)dev);
-    const int64_t need = (int64_t)api.workspace_bytes((int32_t)hq, cache, &where, max_rows);
+    const int64_t need = (int64_t)bytes((int32_t)hq, cache, &where, max_rows);
     const int64_t have = ws.workspace(v[12], need, on);
     const double scale = v[6] == Py_None ? 1.0 / std::sqrt((double)d) : real(v[6]);
-    const int e = api.paged(&qh, (int32_t)hq, code, cache, &where, max_rows, (float)scale, PyObject_IsTrue(v[7]), window, o.data,
+    const int e = call(&qh, (int32_t)hq, code, cache, &where, max_rows, (float)scale, PyObject_IsTrue(v[7]), window, o.data,
                             (float *)lse.data, ws.data, (size_t)have, (int32_t *)st.data, on.raw());
     if (e) return PyLong_FromLong(e);
   }
   return answer({{"out", &o}, {"lse", &lse}, {"status", &st}, {"workspace", &ws}});
+}
+
+PyObject *paged(PyObject *const *v) { return paged_over<dspark_cache>(v, api.workspace_bytes, api.paged); }
+PyObject *paged_byte(PyObject *const *v) {
+  return paged_over<dspark_byte_cache>(v, api.paged_byte_workspace_bytes, api.paged_byte);
 }
 
 // q, k, v, row_off, kv_off, scale, causal, window, want_lse, out, workspace, status, stream
@@ -489,9 +497,10 @@ PyObject *init(PyObject *const *v) {
 }
 
 #define ENTRY(f, n) {#f, (PyCFunction)(void (*)(void))entry<f, n>, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(init, 10),   ENTRY(norm_rope, 10), ENTRY(append, 16),
+PyMethodDef methods[] = {ENTRY(init, 12),   ENTRY(norm_rope, 10), ENTRY(append, 16),
                          ENTRY(read, 9),   ENTRY(paged, 15),     ENTRY(penalize, 15),
-                         ENTRY(prompt, 13), ENTRY(append_byte, 16), ENTRY(read_byte, 10), {}};
+                         ENTRY(prompt, 13), ENTRY(append_byte, 16), ENTRY(read_byte, 10),
+                         ENTRY(paged_byte, 15), {}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};
 
 }  // namespace

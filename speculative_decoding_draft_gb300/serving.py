@@ -66,12 +66,15 @@ def declare(L) -> None:
             ("dspark_attn_prompt", [H, H, H, i64, i64, i64, i32, i32, i32, i32, P, P, f, i32, i64, P, P, P,
                                     ctypes.c_size_t, P, P]),
             ("dspark_attn_append_byte", [H, H, H, i32, i32, C8, W, P, R, P, P, f, P, P, P]),
-            ("dspark_attn_cache_read_byte", [C8, W, i32, P, P, P, P])):
+            ("dspark_attn_cache_read_byte", [C8, W, i32, P, P, P, P]),
+            ("dspark_attn_paged_byte", [H, i32, i32, C8, W, i64, f, i32, i64, P, P, P, ctypes.c_size_t, P, P])):
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
     L.dspark_attn_paged_workspace_bytes.argtypes = [i32, C, W, i64]
     L.dspark_attn_paged_workspace_bytes.restype = ctypes.c_size_t
+    L.dspark_attn_paged_byte_workspace_bytes.argtypes = [i32, C8, W, i64]
+    L.dspark_attn_paged_byte_workspace_bytes.restype = ctypes.c_size_t
     L.dspark_attn_prompt_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32]
     L.dspark_attn_prompt_workspace_bytes.restype = ctypes.c_size_t
 
@@ -93,7 +96,7 @@ def _native():
             "dspark_attn_norm_rope", "dspark_attn_append", "dspark_attn_cache_read",
             "dspark_attn_paged_workspace_bytes", "dspark_attn_paged", "dspark_logits_penalize",
             "dspark_attn_prompt_workspace_bytes", "dspark_attn_prompt", "dspark_attn_append_byte",
-            "dspark_attn_cache_read_byte")))
+            "dspark_attn_cache_read_byte", "dspark_attn_paged_byte_workspace_bytes", "dspark_attn_paged_byte")))
         _binding = native
     return _binding
 
@@ -312,11 +315,11 @@ def cache_read(cache, row_off, kv_len, page_table, rows: int, *, dtype: Optional
                  "dspark_attn_cache_read")
 
 
-def attend_paged(q, cache: PagedCache, row_off, kv_len, page_table, *, scale: Optional[float] = None,
+def attend_paged(q, cache, row_off, kv_len, page_table, *, scale: Optional[float] = None,
                  causal: bool = True, window: int = 0, max_rows: Optional[int] = None, want_lse: bool = False,
                  out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
                  status: Optional[torch.Tensor] = None, stream=None) -> dict:
-    """Attention of ragged rows over the cache (C ABI dspark_attn_paged).
+    """Attention of ragged rows over the cache (C ABI dspark_attn_paged; over a PagedCache8 dspark_attn_paged_byte).
 
     q [rows, Hq, D] bfloat16 or float16 (rows and heads may be strided), Hq a multiple of the cache's heads;
     scale: 1/sqrt(D) unless given.  Row j of request r sees its tokens up to itself (causal) or all kv_len[r], and
@@ -325,7 +328,10 @@ def attend_paged(q, cache: PagedCache, row_off, kv_len, page_table, *, scale: Op
     most rows of a request (default: what ``rows`` allows; smaller is faster).  Returns out [rows, Hq, D] and,
     with want_lse, lse [rows, Hq] float32.
     """
-    _of(cache, PagedCache, "cache")
+    _of(cache, (PagedCache, PagedCache8), "cache")
+    if isinstance(cache, PagedCache8):
+        return _done(_native().paged_byte(q, cache._at, cache.device, row_off, kv_len, page_table, scale, causal, window,
+                                          max_rows, want_lse, out, workspace, status, _raw(stream)), "dspark_attn_paged_byte")
     return _done(_native().paged(q, cache._at, cache.device, row_off, kv_len, page_table, scale, causal, window, max_rows,
                                  want_lse, out, workspace, status, _raw(stream)), "dspark_attn_paged")
 
