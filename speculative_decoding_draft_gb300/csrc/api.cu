@@ -838,7 +838,8 @@ static dspark_status check_byte_attend(int32_t q_heads, const dspark_byte_cache 
   dspark_status st = check_byte_cache(cache);
   if (st == DSPARK_OK) st = check_ragged(where, cache->page_size);
   if (st != DSPARK_OK) return st;
-  // a request's row-heads are 32-bit inside the kernel
+  // steps of 128 tokens, two ahead of the last, are counted in 32 bits
+  if (where->max_pages * cache->page_size > kMaxRows - 1024) return DSPARK_ERR_DIMS;
   if (q_heads < 1 || q_heads > kMaxHeads || q_heads % cache->kv_heads || max_rows < 1 || max_rows > (1 << 20)) return DSPARK_ERR_DIMS;
   return DSPARK_OK;
 }

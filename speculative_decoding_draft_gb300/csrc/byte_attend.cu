@@ -25,9 +25,9 @@
 // CTAs fit on the GPU: lengths need not be alike for all to end together, and one long request fills the GPU by
 // itself.  A unit that is cut leaves its pieces' sums in a workspace, where join_kernel adds them in order.
 //
-// Warps 0-3: a thread has a token of S^T (scales, mask, exponentials, terms of P), then a dimension of O^T.  Warp 4
-// brings keys and values by bulk copies into a ring, looking up pages a step ahead.  Warp 5 issues the products: S
-// of the next step before P V of this one.
+// Warps 0-3 and 4-7: half of the row-heads each; a thread has a token of S^T (scales, mask, exponentials, terms of P),
+// then a dimension of O^T.  Warp 8 brings keys and values by bulk copies into a ring, looking up pages a step ahead.
+// Warp 9 issues the products: S of the next step before P V of this one.
 #include "attn.cuh"
 #include "tcgen05.cuh"
 
@@ -35,7 +35,7 @@ namespace dspark {
 namespace {
 
 constexpr int kTokens = 128;
-constexpr int kThreads = 6 * 32;
+constexpr int kThreads = 10 * 32;
 constexpr float kTop = 11.5f, kBar = 15.5f;      // log2 of where the largest product is put, and may rise to
 constexpr float kNone = 1e30f;                   // the offset of a row-head without a reference: every score passes
 
@@ -85,24 +85,36 @@ __device__ __forceinline__ uint64_t rows_desc(uint32_t addr, int wide) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)((8 * wide) >> 4) << 32) | (1ull << 46) |
          ((wide == 128 ? 2ull : 4ull) << 61);
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr));
+// Columns of the warp's 32 lanes of tensor memory.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait16(uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
-                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+               ::"memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               ::"memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+               : "memory");
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t c;
@@ -127,21 +139,26 @@ __device__ __forceinline__ void terms_of(uint32_t h, uint32_t (&w)[TERMS]) {
     }
   }
 }
-// The 128 threads of warps 0-3 meet, each warp together.
-__device__ __forceinline__ void sync_tokens() {
+// The threads of warps 0-7 meet, each warp together; those of one half of the row-heads; the same and whether one of
+// them says so.
+__device__ __forceinline__ void sync_all() {
   __syncwarp();
-  asm volatile("bar.sync 1, 128;" ::: "memory");
+  asm volatile("bar.sync 1, 256;" ::: "memory");
 }
-__device__ __forceinline__ bool any_token(bool p) {
+__device__ __forceinline__ void sync_half(int half) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 128;" ::"r"(2 + half) : "memory");
+}
+__device__ __forceinline__ bool any_of_half(int half, bool p) {
   uint32_t r;
   __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 2, 128, p;\n\t"
+      "bar.red.or.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)p)
+      : "r"((uint32_t)p), "r"(4 + half)
       : "memory");
   return r != 0;
 }
@@ -227,9 +244,9 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
     }
     mbar_init(smem_u32(&sh.s_full[0]), 1);
     mbar_init(smem_u32(&sh.s_full[1]), 1);
-    mbar_init(smem_u32(&sh.p_full), 4);
+    mbar_init(smem_u32(&sh.p_full), 8);
     mbar_init(smem_u32(&sh.o_done), 1);
-    mbar_init(smem_u32(&sh.q_ready), 4);
+    mbar_init(smem_u32(&sh.q_ready), 8);
     mbar_init(smem_u32(&sh.drain), 1);
     fence_barrier_init();
     sh.begin_request = -1;
@@ -267,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
     if (tid == 0) a.headers[k] = make_int4(-1, 0, 0, 0);
     return;
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(smem_u32(&sh.tmem), Sh::kAlloc);
     tmem_relinquish();
   }
@@ -279,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
   Walk<N> walk;
   walk.start(a, sh.begin_request, sh.begin_at, to - from);
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ---------------- keys and values: K of the first step, then K of the next and V of each ----------------
     int idx = 0;
     bool ok = true;
@@ -331,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
         }
       }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ---------------- products ----------------
     if (lane == 0) {
       int idx = 0, step = 0, piece = 0;
@@ -382,8 +399,10 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
     __syncwarp();
   } else {
     // ---------------- scores to probabilities, sums to outputs ----------------
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    const int dim = D == 128 ? tid : warp * 16 + lane;           // of O^T: with 64 dimensions 16 lanes of each warp
+    constexpr int NC = N / 2, kStep = NC < 16 ? 8 : 16;          // row-heads of a half, at once out of tensor memory
+    const int half = warp >> 2, col0 = half * NC, quad = warp & 3, t = tid & 127;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const int dim = D == 128 ? t : quad * 16 + lane;             // of O^T: with 64 dimensions 16 lanes of each warp
     const bool has_dim = D == 128 || lane < 16;
     const uint32_t p_at = sb + Sh::kOffP;
     int step = 0, idx = 0;
@@ -395,9 +414,9 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
       const int hi_min = a.causal ? ctx + first / a.group + 1 : q.kv;
       const int hi_max = a.causal ? ctx + (first + real - 1) / a.group + 1 : q.kv;
       const int lo_min = a.window ? max(hi_min, a.window) - a.window : 0, lo_max = a.window ? max(hi_max, a.window) - a.window : 0;
-      sync_tokens();                                             // (the last piece's sums have been read)
+      sync_all();                                                // (the last piece's sums have been read)
       // queries: 128 / N threads a row-head
-      {
+      if (half == 0) {
         constexpr int kEach = 128 / N, kPieces = D / kEach / 8;
         const int c = tid / kEach, part = tid % kEach, rho = first + c;
         float x[kPieces * 8];
@@ -445,144 +464,163 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
         if (tid == 0) sh.odd = 0;
       }
       fence_proxy_async_smem();
-      sync_tokens();
+      sync_all();
       const bool some = walk.ca < walk.cb;
       if (some && lane == 0) mbar_arrive(smem_u32(&sh.q_ready));
       __syncwarp();
-      float l[N];
+      float l[NC];
 #pragma unroll
-      for (int c = 0; c < N; ++c) l[c] = 0.0f;
+      for (int c = 0; c < NC; ++c) l[c] = 0.0f;
 
-      // the scales of the thread's token, a step ahead, its page two
+      // The scales of the thread's token, a step ahead, and its page, two.  Its place (page of the text, token of the
+      // page) moves on by the same numbers every step.
       const int32_t *table = a.table + walk.r * a.max_pages;
-      const int blocks = a.page_size / kTileTokens;
-      auto page_of = [&](int c) -> int32_t {
-        const int t = c * kTokens + tid;
-        const int32_t p = c < walk.cb && t >= lo_min && t < hi_max ? table[t / a.page_size] : -1;
-        return p < a.pages ? p : -1;
-      };
-      auto scales_at = [&](int c, int32_t page, uint32_t &ks, uint32_t &vs) {
-        ks = vs = 127;
-        if (page < 0) return;
-        const uint8_t *s = a.scales + ((int64_t)page * a.Hkv + walk.h) * 2 * blocks + (c * kTokens + tid) % a.page_size / kTileTokens;
-        ks = s[0], vs = s[blocks];
+      const int blocks = a.page_size / kTileTokens, pages_on = kTokens / a.page_size, tokens_on = kTokens - pages_on * a.page_size;
+      int at_page = (walk.ca * kTokens + t) / a.page_size, in_page = walk.ca * kTokens + t - at_page * a.page_size, at = walk.ca * kTokens + t;
+      int32_t page = -1;
+      int block = 0;
+      auto look_up = [&]() {                                     // page and block of the token `at`; on to the next step's
+        page = at < walk.cb * kTokens && at >= lo_min && at < hi_max ? table[at_page] : -1;
+        block = in_page / kTileTokens;
+        at += kTokens, at_page += pages_on, in_page += tokens_on;
+        if (in_page >= a.page_size) in_page -= a.page_size, ++at_page;
       };
       uint32_t ks = 127, vs = 127;
-      int32_t page = page_of(walk.ca);
-      scales_at(walk.ca, page, ks, vs);
-      page = page_of(walk.ca + 1);
+      auto load_scales = [&]() {
+        ks = vs = 127;
+        if (page >= 0 && page < a.pages) {
+          const uint8_t *s = a.scales + ((int64_t)page * a.Hkv + walk.h) * 2 * blocks + block;
+          ks = s[0], vs = s[blocks];
+        }
+      };
+      look_up();
+      load_scales();
+      look_up();
       // where V of a step lies in the ring: K0, K1, V0, K2, V1, ...
       for (int c = walk.ca; c < walk.cb; ++c, ++step) {
         const bool at_first = c == walk.ca;
         const int v_idx = idx + (c + 1 < walk.cb ? (at_first ? 2 : 1) : (at_first ? 1 : 0));
         idx = v_idx + 1;
         const float A = scale_of(ks), w = scale_of(vs), lw = (float)((int)min(max(vs, 95u), 158u) - 127);
-        scales_at(c + 1, page, ks, vs);
-        page = page_of(c + 2);
-        const int base = c * kTokens, tok = base + tid;
+        load_scales();
+        look_up();
+        const int base = c * kTokens, tok = base + t;
         const bool edge = base < lo_max || base + kTokens > hi_min;
         const bool mine_ok = mbar_wait(smem_u32(&sh.s_full[step & 1]), (uint32_t)(step >> 1 & 1), abort);
         alive = __all_sync(0xffffffffu, mine_ok) && alive;
         tc_fence_after();
-        unsigned long long y[N / 2];
+        unsigned long long y[NC / 2];
         {
           const unsigned long long A2 = f2_pack(A, A);
-          uint32_t s[N / 16][16];
+          uint32_t s[NC / kStep][kStep];
 #pragma unroll
-          for (int b = 0; b < N / 16; ++b) tmem_ld16(tmem + lanes + (step & 1) * N + b * 16, s[b]);
+          for (int b = 0; b < NC / kStep; ++b) tmem_ld(tmem + lanes + (step & 1) * N + col0 + b * kStep, s[b]);
 #pragma unroll
-          for (int b = 0; b < N / 16; ++b) {
-            tmem_wait16(s[b]);
+          for (int b = 0; b < NC / kStep; ++b) {
+            tmem_wait(s[b]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[b * 8 + j] = f2_mul(f2_pack(__uint_as_float(s[b][2 * j]), __uint_as_float(s[b][2 * j + 1])), A2);
+            for (int j = 0; j < kStep / 2; ++j)
+              y[b * kStep / 2 + j] = f2_mul(f2_pack(__uint_as_float(s[b][2 * j]), __uint_as_float(s[b][2 * j + 1])), A2);
           }
         }
         if (edge) {
 #pragma unroll
-          for (int j = 0; j < N / 2; ++j) {
+          for (int j = 0; j < NC / 2; ++j) {
             float y0, y1;
             f2_unpack(y[j], y0, y1);
-            const int h0 = sh.hi[2 * j], h1 = sh.hi[2 * j + 1];
+            const int h0 = sh.hi[col0 + 2 * j], h1 = sh.hi[col0 + 2 * j + 1];
             if (!(tok < h0 && (!a.window || tok >= h0 - a.window))) y0 = -INFINITY;
             if (!(tok < h1 && (!a.window || tok >= h1 - a.window))) y1 = -INFINITY;
             y[j] = f2_pack(y0, y1);
           }
         }
-        const ulonglong2 *Rs = reinterpret_cast<const ulonglong2 *>(sh.R), *zs = reinterpret_cast<const ulonglong2 *>(sh.z);
-        float most = -INFINITY;
+        const ulonglong2 *Rs = reinterpret_cast<const ulonglong2 *>(sh.R + col0), *zs = reinterpret_cast<const ulonglong2 *>(sh.z + col0);
+        unsigned long long e[NC / 2];                            // exponents of the probabilities
+        auto exponents = [&]() {
+          float most = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < N / 4; ++j) {
-          const ulonglong2 r2 = Rs[j], z2 = zs[j];
-          float x0, x1, x2, x3;
-          f2_unpack(f2_fma(y[2 * j], r2.x, z2.x), x0, x1);
-          f2_unpack(f2_fma(y[2 * j + 1], r2.y, z2.y), x2, x3);
-          most = fmaxf(fmaxf(most, fmaxf(x0, x1)), fmaxf(x2, x3));
-        }
-        if (any_token(most + lw > kBar)) {                       // a reference moves
+          for (int j = 0; j < NC / 4; ++j) {
+            const ulonglong2 r2 = Rs[j], z2 = zs[j];
+            float x0, x1, x2, x3;
+            e[2 * j] = f2_fma(y[2 * j], r2.x, z2.x);
+            e[2 * j + 1] = f2_fma(y[2 * j + 1], r2.y, z2.y);
+            f2_unpack(e[2 * j], x0, x1);
+            f2_unpack(e[2 * j + 1], x2, x3);
+            most = fmaxf(fmaxf(most, fmaxf(x0, x1)), fmaxf(x2, x3));
+          }
+          return most;
+        };
+        if (any_of_half(half, exponents() + lw > kBar)) {        // a reference moves
 #pragma unroll
-          for (int j = 0; j < N / 2; ++j) {
+          for (int j = 0; j < NC / 2; ++j) {
             float y0, y1;
             f2_unpack(y[j], y0, y1);
-            float m[2] = {fmaf(y0, sh.R[2 * j], lw), fmaf(y1, sh.R[2 * j + 1], lw)};
+            const int c2 = col0 + 2 * j;
+            float m2[2] = {fmaf(y0, sh.R[c2], lw), fmaf(y1, sh.R[c2 + 1], lw)};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float x = m[i] == m[i] ? m[i] : -INFINITY;
+              float x = m2[i] == m2[i] ? m2[i] : -INFINITY;
 #pragma unroll
               for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-              if (lane == 0) sh.most[warp][2 * j + i] = x;
+              if (lane == 0) sh.most[quad][c2 + i] = x;
             }
           }
-          sync_tokens();
-          if (tid < N) {
-            const float was = sh.ref[tid];
-            const float up = fmaxf(fmaxf(fmaxf(sh.most[0][tid], sh.most[1][tid]), fmaxf(sh.most[2][tid], sh.most[3][tid])), was);
-            sh.factor[tid] = was == -INFINITY ? 0.0f : fast_ex2(was - up);
-            sh.ref[tid] = up;
-            if (up != -INFINITY && tid < real) sh.z[tid] = kTop - up;
+          sync_half(half);
+          if (t < NC) {
+            const int c2 = col0 + t;
+            const float was = sh.ref[c2];
+            const float up = fmaxf(fmaxf(fmaxf(sh.most[0][c2], sh.most[1][c2]), fmaxf(sh.most[2][c2], sh.most[3][c2])), was);
+            sh.factor[c2] = was == -INFINITY ? 0.0f : fast_ex2(was - up);
+            sh.ref[c2] = up;
+            if (up != -INFINITY && c2 < real) sh.z[c2] = kTop - up;
           }
-          sync_tokens();
+          sync_half(half);
 #pragma unroll
-          for (int c2 = 0; c2 < N; ++c2) l[c2] *= sh.factor[c2];
+          for (int c2 = 0; c2 < NC; ++c2) l[c2] *= sh.factor[col0 + c2];
           if (!at_first) {
             const bool done = mbar_wait(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1), abort);
             alive = __all_sync(0xffffffffu, done) && alive;
             tc_fence_after();
-            for (int b = 0; b < kTerms * N / 16; ++b) {
-              uint32_t o[16];
-              tmem_ld16(o_tmem + lanes + b * 16, o);
-              tmem_wait16(o);
+#pragma unroll 1
+            for (int i = 0; i < kTerms; ++i)
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.factor[(b * 16 + j) % N]);
-              tmem_st16(o_tmem + lanes + b * 16, o);
-            }
+              for (int b = 0; b < NC / kStep; ++b) {
+                const uint32_t o_at = o_tmem + lanes + i * N + col0 + b * kStep;
+                uint32_t o[kStep];
+                tmem_ld(o_at, o);
+                tmem_wait(o);
+#pragma unroll
+                for (int j = 0; j < kStep; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.factor[col0 + b * kStep + j]);
+                tmem_st(o_at, o);
+              }
             tmem_wait_st();
             tc_fence_before();
           }
+          exponents();
         }
-        // probabilities in terms; the place of a byte in P: row 128, its 16-byte piece swizzled by the row
+        // probabilities in terms; the place of a byte in P: a row of 128, its 16-byte piece swizzled by the row
         if (!at_first) {
           const bool done = mbar_wait(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1), abort);
           alive = __all_sync(0xffffffffu, done) && alive;
         }
         const unsigned long long w2 = f2_pack(w, w);
+        const uint32_t p_col = p_at + col0 * kTokens;
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-          const ulonglong2 r2 = Rs[j / 2], z2 = zs[j / 2];
+        for (int j = 0; j < NC / 2; ++j) {
           float x0, x1;
-          f2_unpack(f2_fma(y[j], j & 1 ? r2.y : r2.x, j & 1 ? z2.y : z2.x), x0, x1);
+          f2_unpack(e[j], x0, x1);
           const float p0 = fast_ex2(x0), p1 = fast_ex2(x1);
           l[2 * j] += p0;
           l[2 * j + 1] += p1;
           float v0, v1;
           f2_unpack(f2_mul(f2_pack(p0, p1), w2), v0, v1);
-          uint32_t t[kTerms];
-          terms_of<kTerms, true>(pack_half2(v0, v1), t);
+          uint32_t x[kTerms];
+          terms_of<kTerms, true>(pack_half2(v0, v1), x);
+          const uint32_t to0 = p_col + (t ^ ((2 * j & 7) << 4)), to1 = p_col + (t ^ (((2 * j + 1) & 7) << 4));
 #pragma unroll
           for (int i = 0; i < kTerms; ++i) {
-            const uint32_t to0 = p_at + (i * N + 2 * j) * kTokens + (tid ^ ((2 * j & 7) << 4));
-            const uint32_t to1 = p_at + (i * N + 2 * j + 1) * kTokens + (tid ^ (((2 * j + 1) & 7) << 4));
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(to0), "r"(t[i] >> 8) : "memory");
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(to1), "r"(t[i] >> 24) : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(to0 + (i * N + 2 * j) * kTokens), "r"(x[i] >> 8) : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(to1 + (i * N + 2 * j + 1) * kTokens), "r"(x[i] >> 24) : "memory");
           }
         }
         if (edge) {
@@ -592,10 +630,10 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
           const int s = v_idx % kSlots;
           const bool there = mbar_wait(full + 8 * s, (uint32_t)(v_idx / kSlots & 1), abort);
           alive = __all_sync(0xffffffffu, there) && alive;
-          uint4 *v = reinterpret_cast<uint4 *>(gb + s * Sh::kSlot + tid * D);
+          uint4 *v = reinterpret_cast<uint4 *>(gb + s * Sh::kSlot + t * D) + half * (D / 32);   // half of the value each
           const bool seen = tok >= lo_min && tok < hi_max;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
+          for (int i = 0; i < D / 32; ++i) {
             uint4 x = v[i];
             if (!seen) {
               v[i] = make_uint4(0, 0, 0, 0);
@@ -629,13 +667,13 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
         tc_fence_after();
       }
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
+      for (int c = 0; c < NC; ++c) {
         float x = l[c];
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        if (lane == 0) sh.sum[warp][c] = x;
+        if (lane == 0) sh.sum[quad][col0 + c] = x;
       }
-      sync_tokens();
+      sync_all();
       const bool whole = walk.begins && walk.ends, odd = *(volatile int *)&sh.odd != 0;
       float *partial = a.partial + (2 * k + (walk.begins ? 1 : 0)) * Sh::kPartial;
       if (!whole && tid < N) {
@@ -643,43 +681,45 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
         partial[N + tid] = sh.sum[0][tid] + sh.sum[1][tid] + sh.sum[2][tid] + sh.sum[3][tid];
       }
       __syncwarp();
-      for (int b = 0; b < N / 16; ++b) {
-        if (b * 16 >= real) break;
-        float y[16];
+#pragma unroll 1
+      for (int b = 0; b < NC / kStep; ++b) {
+        const int c0 = col0 + b * kStep;
+        if (c0 >= real) break;
+        float y[kStep];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = 0.0f;
+        for (int j = 0; j < kStep; ++j) y[j] = 0.0f;
         if (some) {
 #pragma unroll
           for (int i = 0; i < kTerms; ++i) {
-            uint32_t o[16];
-            tmem_ld16(o_tmem + lanes + i * N + b * 16, o);
-            tmem_wait16(o);
+            uint32_t o[kStep];
+            tmem_ld(o_tmem + lanes + i * N + c0, o);
+            tmem_wait(o);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] += __uint_as_float(o[j]);
+            for (int j = 0; j < kStep; ++j) y[j] += __uint_as_float(o[j]);
           }
         }
         if (odd && has_dim)
           for (int c = walk.ca; c < walk.cb; ++c) {
             if (!(c * kTokens < lo_max || c * kTokens + kTokens > hi_min)) continue;
-            for (int t = max(c * kTokens, lo_min); t < min(c * kTokens + kTokens, hi_max); ++t) {
-              const int32_t pg = table[t / a.page_size];
+            for (int x = max(c * kTokens, lo_min); x < min(c * kTokens + kTokens, hi_max); ++x) {
+              const int32_t pg = table[x / a.page_size];
               if (pg < 0 || pg >= a.pages) continue;
-              const int in = t % a.page_size, piece = D == 128 ? (dim / 16) ^ (in & 7) : (dim / 16) ^ ((in >> 1) & 3);
-              const uint8_t e = a.data[((((int64_t)pg * a.Hkv + walk.h) * 2 + 1) * a.page_size + in) * D + piece * 16 + dim % 16];
-              if ((e & 0x7f) != 0x7f) continue;
+              const int in = x % a.page_size, piece = D == 128 ? (dim / 16) ^ (in & 7) : (dim / 16) ^ ((in >> 1) & 3);
+              const uint8_t held = a.data[((((int64_t)pg * a.Hkv + walk.h) * 2 + 1) * a.page_size + in) * D + piece * 16 + dim % 16];
+              if ((held & 0x7f) != 0x7f) continue;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int hi = sh.hi[b * 16 + j];
-                if (t < hi && (!a.window || t >= hi - a.window)) y[j] = __int_as_float(0x7fffffff);
+              for (int j = 0; j < kStep; ++j) {
+                const int hi = sh.hi[c0 + j];
+                if (x < hi && (!a.window || x >= hi - a.window)) y[j] = __int_as_float(0x7fffffff);
               }
             }
           }
         __syncwarp();
         if (alive && has_dim) {
-          int tok = (first + b * 16) / a.group, sub = first + b * 16 - tok * a.group;
+          int tok = (first + c0) / a.group, sub = first + c0 - tok * a.group;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int c = b * 16 + j;
+          for (int j = 0; j < kStep; ++j) {
+            const int c = c0 + j;
             if (c >= real) break;
             if (whole) {
               const float sum = sh.sum[0][c] + sh.sum[1][c] + sh.sum[2][c] + sh.sum[3][c];
@@ -706,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) tmem_dealloc(tmem, Sh::kAlloc);
+  if (warp == 9) tmem_dealloc(tmem, Sh::kAlloc);
 }
 
 // Joins the pieces of the unit that began in CTA blockIdx.x / groups and went on: a warp takes a row-head.

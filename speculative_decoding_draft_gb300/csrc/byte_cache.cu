@@ -9,8 +9,9 @@
 //
 // A run is the rows of one call that fall into one block: up to 16.  A CTA takes the runs that begin in a window of rows
 // (its heads shared out over `parts` CTAs where rows are few): 8 warps make the angles of the run's rows once for
-// all heads, then a warp takes the keys or the values of one head, all rows of the run in registers, since the scale
-// is known only when all of them are; queries go row by row.  A lane holds 8 neighbouring dimensions.
+// all heads, then a warp takes the keys or the values of one head, twice over the rows of the run, since the scale is
+// known only when all of them are (held in registers between the two, 16 rows took 128 registers a thread, and
+// half the warps on an SM); queries go row by row.  A lane holds 8 neighbouring dimensions.
 //
 // All arithmetic is in fp32; queries are rounded once to their type, keys and values once to 8 bits, and once more
 // where a block's scale rises behind them.
@@ -55,10 +56,10 @@ __device__ __forceinline__ Eight<DT> load8_once(const void *p) {
 }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(kThreads, DT == DSPARK_F32 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, 3)
     append_kernel(const __grid_constant__ ByteHeadsArgs a, int window, int parts) {
   using T = typename Elem<DT>::T;
-  constexpr int LANES = D / 8, kBeside = 32 / LANES, kPasses = kTileTokens / kBeside;
+  constexpr int LANES = D / 8, kBeside = 32 / LANES, kAhead = DT == DSPARK_F32 ? 2 : 4;
   __shared__ __align__(16) float C[kTileTokens][D], S[kTileTokens][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES, beside = lane / LANES;
   const int64_t first = blockIdx.x / (unsigned)parts * (int64_t)window;
@@ -181,51 +182,54 @@ __global__ void __launch_bounds__(kThreads, DT == DSPARK_F32 ? 1 : 2)
       uint8_t *scale_at = a.scales + block * per + in_page;
       uint8_t *data = a.data + (block * a.page_size + in_page * kTileTokens) * D;
       const int held = t0 ? exponent_held(*scale_at) : kELow;
-      Pair x[kPasses][4];
-      Eight<DT> in[kPasses];
+      // twice over the rows: for the largest magnitude, then for the elements (what is read again lies in the caches)
+      auto sweep = [&](auto &&use) {
+#pragma unroll 1
+        for (int p0 = 0; p0 < len; p0 += kAhead * kBeside) {
+          Eight<DT> in[kAhead];
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        const int j = p * kBeside + beside;
-        if (p * kBeside < len) in[p] = j < len ? load8_once<DT>(src + j * src_row) : Eight<DT>{};
-      }
+          for (int p = 0; p < kAhead; ++p) {
+            const int j = p0 + p * kBeside + beside;
+            in[p] = j < len ? load8<DT>(src, j * src_row) : Eight<DT>{};
+          }
+#pragma unroll
+          for (int p = 0; p < kAhead; ++p) {
+            if (p0 + p * kBeside >= len) break;
+            const int j = p0 + p * kBeside + beside;
+            Pair x[4];
+            to_pairs<DT>(in[p], x);
+            if (!kind) turn(x, a.k_weight != nullptr, w1, min(j, len - 1));
+            if (j < len) use(x, j);
+          }
+        }
+      };
       float top = 0.0f;
+      sweep([&](const Pair (&x)[4], int) {
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        if (p * kBeside >= len) break;
-        to_pairs<DT>(in[p], x[p]);
-        if (!kind) turn(x[p], a.k_weight != nullptr, w1, min(p * kBeside + beside, len - 1));
-        if (p * kBeside + beside < len)
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = floats_of(x[e]);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));             // a NaN counts nothing
+        }
+      });
+      uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+      if (bits >= 0x7f800000u) {                                                  // infinities count nothing either
+        top = 0.0f;
+        sweep([&](const Pair (&x)[4], int) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 f = floats_of(x[p][e]);
-            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));           // a NaN counts nothing
+            const float2 f = floats_of(x[e]);
+            if (fabsf(f.x) < INFINITY) top = fmaxf(top, fabsf(f.x));
+            if (fabsf(f.y) < INFINITY) top = fmaxf(top, fabsf(f.y));
           }
-      }
-      uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      if (bits >= 0x7f800000u) {                       // infinities count nothing either
-        top = 0.0f;
-#pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-          if (p * kBeside >= len) break;
-          if (p * kBeside + beside < len)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = floats_of(x[p][e]);
-              if (fabsf(f.x) < INFINITY) top = fmaxf(top, fabsf(f.x));
-              if (fabsf(f.y) < INFINITY) top = fmaxf(top, fabsf(f.y));
-            }
-        }
+        });
         bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
       }
       const int e = max(held, exponent_for(bits));
       const float unit = two_to(-e);
-#pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        if (p * kBeside >= len) break;
-        const int j = p * kBeside + beside, t = t0 + j;
-        if (j < len)
-          *reinterpret_cast<uint2 *>(data + t * D + piece_at<D>(t, sub >> 1) * 16 + (sub & 1) * 8) = elements(x[p], unit);
-      }
+      sweep([&](const Pair (&x)[4], int j) {
+        const int t = t0 + j;
+        *reinterpret_cast<uint2 *>(data + t * D + piece_at<D>(t, sub >> 1) * 16 + (sub & 1) * 8) = elements(x, unit);
+      });
       if (t0 && e > held) {                            // what the block holds already, on the new scale
         const float down = two_to(held - e);
         for (int i = lane; i < t0 * (D / 8); i += 32) {

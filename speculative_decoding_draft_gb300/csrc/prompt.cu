@@ -141,6 +141,51 @@ __device__ __forceinline__ int64_t request_of_unit(const int32_t *row_off, int64
   return lo;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// A step's scores as probabilities 2^(s R + z) in 16 bits, their sum and the largest exponent.  The next 32 scores are on
+// their way while 32 are worked on.  EDGE: only columns lo .. hi - 1 are seen, and those from `cols` on not looked at.
+template <int DT, bool EDGE>
+__device__ __forceinline__ void take_step(uint32_t s_at, int cols, int lo, int hi, float R, float z, uint32_t (&P)[64],
+                                          float &most, float &sum) {
+  const unsigned long long R2 = f2_pack(R, R), z2 = f2_pack(z, z);
+  unsigned long long total[2] = {0, 0};
+  float top[2] = {-INFINITY, -INFINITY};
+  uint32_t s[2][32];
+  tmem_ld32(s_at, s[0]);
+  tmem_wait_ld(s[0]);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    if (EDGE && b * 32 >= cols) break;
+    if (b < 3 && (!EDGE || b * 32 + 32 < cols)) tmem_ld32(s_at + b * 32 + 32, s[(b + 1) & 1]);
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const int i = k / 2 & 1;
+      float x0, x1;
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(s[b & 1][k]), __uint_as_float(s[b & 1][k + 1])), R2, z2), x0, x1);
+      if (EDGE) {
+        const int tok = b * 32 + k;
+        if (!(tok < hi && tok >= lo)) x0 = -INFINITY;
+        if (!(tok + 1 < hi && tok + 1 >= lo)) x1 = -INFINITY;
+      }
+      top[i] = max3(top[i], x0, x1);
+      const float p0 = fast_ex2(x0), p1 = fast_ex2(x1);
+      total[i] = f2_add(total[i], f2_pack(p0, p1));
+      P[b * 16 + k / 2] = pack_pair<DT>(p0, p1);
+    }
+    if (EDGE) __syncwarp();
+    if (b < 3 && (!EDGE || b * 32 + 32 < cols)) tmem_wait_ld(s[(b + 1) & 1]);
+  }
+  most = fmaxf(top[0], top[1]);
+  float t0, t1;
+  f2_unpack(f2_add(total[0], total[1]), t0, t1);
+  sum = t0 + t1;
+}
+
 template <int DT, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap k_map,
@@ -454,31 +499,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           }
-          float most = -INFINITY;
-          float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            if (b * 32 >= cols) break;
-            uint32_t s[32];
-            tmem_ld32(s_at + b * 32, s);
-            tmem_wait_ld(s);
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const int tok = b * 32 + k;
-              float x0 = fmaf(__uint_as_float(s[k]), R, z), x1 = fmaf(__uint_as_float(s[k + 1]), R, z);
-              if (at_edge) {
-                if (!(tok < hi && tok >= lo)) x0 = -INFINITY;
-                if (!(tok + 1 < hi && tok + 1 >= lo)) x1 = -INFINITY;
-              }
-              most = fmaxf(most, fmaxf(x0, x1));
-              const float p0 = fast_ex2(x0), p1 = fast_ex2(x1);
-              sum0 += p0;
-              sum1 += p1;
-              P[b * 16 + k / 2] = pack_pair<DT>(p0, p1);
-            }
-            __syncwarp();
-          }
-          more = sum0 + sum1;
+          float most;
+          if (at_edge)
+            take_step<DT, true>(s_at, cols, lo, hi, R, z, P, most, more);
+          else
+            take_step<DT, false>(s_at, kTokens, 0, 0, R, z, P, most, more);
           // (a first maximum of -inf leaves the next step to measure; an infinite score measured leaves it at that)
           if (measure || !__any_sync(0xffffffffu, most > kLift + kLazy || (top == -INFINITY && most > -INFINITY))) break;
           measure = true;
