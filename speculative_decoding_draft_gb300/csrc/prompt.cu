@@ -304,31 +304,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 8) {
     // ---------------- products ----------------
-    if (lane == 0 && c0 < c1) {
+    // (the whole warp waits, one lane issues)
+    if (c0 < c1) {
       bool ok = true;
       int fine = 0;                                              // edges whose values have been looked at
-      auto slot_full = [&](int idx) { return mbar_wait(full + 8 * (idx % kSlots), (uint32_t)(idx / kSlots & 1), abort); };
-      auto scores = [&](const Tile &tile, int i, int c, int idx) {   // S of tile i for step c, keys in slot idx
-        const uint32_t k_at = sb + Sh::kOffKv + (idx % kSlots) * Sh::kSlot;
-        const uint32_t idesc = kIdesc | ((uint32_t)(tile.columns(c) >> 3) << 17);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          mma_bf16(tmem + i * 128, smem_desc(sb + i * Sh::kQ + s / 4 * (kTileRows * 128) + s % 4 * 32, 16, 1024),
-                   smem_desc(k_at + s / 4 * (kTokens * 128) + s % 4 * 32, 16, 1024), idesc, s > 0);
-        mma_commit(smem_u32(&sh.s_full[i]));
+      auto wait = [&](uint64_t &bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_try(smem_u32(&bar), parity) || mbar_wait(smem_u32(&bar), parity, abort)) != 0;
       };
-      for (int i = 0; ok && i < tiles; ++i) ok = mbar_wait(smem_u32(&sh.q_full[i]), 0, abort);
+      auto slot_full = [&](int idx) { return wait(sh.full[idx % kSlots], (uint32_t)(idx / kSlots & 1)); };
+      const uint64_t q_desc = smem_desc(sb, 16, 1024), k_desc = smem_desc(sb + Sh::kOffKv, 16, 1024),
+                     v_desc = smem_desc(sb + Sh::kOffKv, kTokens * 128, 1024);
+      auto scores = [&](const Tile &tile, int i, int c, int idx) {   // S of tile i for step c, keys in slot idx
+        const uint64_t k_at = desc_on(k_desc, (idx % kSlots) * Sh::kSlot), q_at = desc_on(q_desc, i * Sh::kQ);
+        const uint32_t idesc = kIdesc | ((uint32_t)(tile.columns(c) >> 3) << 17);
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t on = s / 4 * (kTileRows * 128) + s % 4 * 32;     // (tiles and steps have 128 rows both)
+            mma_bf16(tmem + i * 128, desc_on(q_at, on), desc_on(k_at, on), idesc, s > 0);
+          }
+          mma_commit(smem_u32(&sh.s_full[i]));
+        }
+        __syncwarp();
+      };
+      auto give_back = [&](int idx) {
+        if (elect_one()) mma_commit(empty + 8 * (idx % kSlots));
+        __syncwarp();
+      };
+      for (int i = 0; ok && i < tiles; ++i) ok = wait(sh.q_full[i], 0);
       if (ok) ok = slot_full(0);
       tc_fence_after();
       if (ok) {
         if (tile_a.on(c0)) scores(tile_a, 0, c0, 0);
         if (tile_b.on(c0)) scores(tile_b, 1, c0, 0);
-        mma_commit(empty);
+        give_back(0);
       }
       uint32_t turn[2] = {0, 0};
       for (int c = c0; ok && c < c1; ++c) {
         const int j = c - c0, k_idx = 1 + 2 * j, v_idx = c + 1 < c1 ? 2 + 2 * j : 1 + 2 * j;
-        const uint32_t v_at = sb + Sh::kOffKv + (v_idx % kSlots) * Sh::kSlot;
+        const uint64_t v_at = desc_on(v_desc, (v_idx % kSlots) * Sh::kSlot);
         bool v_there = false, k_there = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -337,20 +351,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!v_there) {
               ok = slot_full(v_idx);
               if (ok && any_edge(c)) {
-                ok = mbar_wait(smem_u32(&sh.v_fine[fine % kSlots]), (uint32_t)(fine / kSlots & 1), abort);
+                ok = wait(sh.v_fine[fine % kSlots], (uint32_t)(fine / kSlots & 1));
                 ++fine;
               }
               v_there = true;
             }
-            if (ok) ok = mbar_wait(smem_u32(&sh.p_full[i]), turn[i], abort);
+            if (ok) ok = wait(sh.p_full[i], turn[i]);
             turn[i] ^= 1;
             if (ok) {
               tc_fence_after();
               const int steps = tile.columns(c) / 16;
-              for (int s = 0; s < steps; ++s)
-                mma_ts(tmem + 256 + i * 128, tmem + i * 128 + s * 8, smem_desc(v_at + s * 2048, kTokens * 128, 1024), kIdescO,
-                       c > tile.t0 || s > 0);
-              if (c + 1 == tile.t1) mma_commit(smem_u32(&sh.o_full[i]));
+              if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < kTokens / 16; ++s)
+                  if (s < steps)
+                    mma_ts(tmem + 256 + i * 128, tmem + i * 128 + s * 8, desc_on(v_at, s * 2048), kIdescO, c > tile.t0 || s > 0);
+                if (c + 1 == tile.t1) mma_commit(smem_u32(&sh.o_full[i]));
+              }
+              __syncwarp();
             }
           }
           if (ok && c + 1 < c1 && tile.on(c + 1)) {
@@ -363,11 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           if (!v_there) ok = slot_full(v_idx);                   // (a step that no tile takes)
           if (ok && c + 1 < c1 && !k_there) ok = slot_full(k_idx);
-          if (c + 1 < c1) mma_commit(empty + 8 * (k_idx % kSlots));
-          mma_commit(empty + 8 * (v_idx % kSlots));
+          if (c + 1 < c1) give_back(k_idx);
+          give_back(v_idx);
         }
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         set_status(a.dev_status, DSPARK_ERR_DEVICE_TIMEOUT);
         mma_commit(smem_u32(&sh.drain));
         const long long begun = clock64();
@@ -447,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t turn = 0;
       bool ok = true;
       for (int c = tile.t0; c < tile.t1; ++c) {
-        ok = mbar_wait(smem_u32(&sh.s_full[i]), turn, abort);
+        ok = mbar_try(smem_u32(&sh.s_full[i]), turn) || mbar_wait(smem_u32(&sh.s_full[i]), turn, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         turn ^= 1;
