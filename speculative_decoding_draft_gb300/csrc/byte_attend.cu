@@ -28,6 +28,8 @@
 // Warps 0-3 and 4-7: half of the row-heads each; a thread has a token of S^T (scales, mask, exponentials, terms of P),
 // then a dimension of O^T.  Warp 8 brings keys and values by bulk copies into a ring, looking up pages a step ahead.
 // Warp 9 issues the products: S of the next step before P V of this one.
+#include <type_traits>
+
 #include "attn.cuh"
 #include "tcgen05.cuh"
 
@@ -99,21 +101,6 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&v)[8]) {
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-               : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_wait(uint32_t (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               ::"memory");
-}
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
                : "memory");
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -350,57 +337,68 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
     __syncwarp();
   } else if (warp == 9) {
     // ---------------- products ----------------
-    if (lane == 0) {
-      int idx = 0, step = 0, piece = 0;
-      bool ok = true;
-      while (ok && walk.next(a)) {
-        if (walk.ca >= walk.cb) continue;
-        ok = mbar_wait(smem_u32(&sh.q_ready), (uint32_t)(piece++ & 1), abort);
-        auto scores = [&](int s_no) {                            // of the keys in the next slot
-          const int s = idx % kSlots;
-          if (!mbar_wait(full + 8 * s, (uint32_t)(idx / kSlots & 1), abort)) return false;
-          tc_fence_after();
-          const uint32_t k_at = sb + s * Sh::kSlot;
+    // (the whole warp waits, one lane issues)
+    int idx = 0, step = 0, piece = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_try(smem_u32(&bar), parity) || mbar_wait(smem_u32(&bar), parity, abort)) != 0;
+    };
+    const uint64_t slots = rows_desc(sb, D), p_desc = rows_desc(sb + Sh::kOffP, 128), q_desc = rows_desc(sb + Sh::kOffQ, D);
+    while (ok && walk.next(a)) {
+      if (walk.ca >= walk.cb) continue;
+      ok = wait(sh.q_ready, (uint32_t)(piece++ & 1));
+      auto scores = [&](int s_no) {                              // of the keys in the next slot
+        const int s = idx % kSlots;
+        if (!wait(sh.full[s], (uint32_t)(idx / kSlots & 1))) return false;
+        tc_fence_after();
+        const uint64_t k_at = desc_on(slots, s * Sh::kSlot);
+        if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kTerms; ++i)
 #pragma unroll
             for (int x = 0; x < D / 32; ++x)
-              mma_f8(tmem + (s_no & 1) * N, rows_desc(k_at + x * 32, D), rows_desc(sb + Sh::kOffQ + i * N * D + x * 32, D), kIdescS, i + x > 0);
+              mma_f8(tmem + (s_no & 1) * N, desc_on(k_at, x * 32), desc_on(q_desc, i * N * D + x * 32), kIdescS, i + x > 0);
           mma_commit(smem_u32(&sh.s_full[s_no & 1]));
           mma_commit(empty + 8 * s);
-          ++idx;
-          return true;
-        };
-        if (ok) ok = scores(step);
-        for (int c = walk.ca; ok && c < walk.cb; ++c, ++step) {
-          if (c + 1 < walk.cb) ok = scores(step + 1);
-          if (ok) ok = mbar_wait(smem_u32(&sh.p_full), (uint32_t)(step & 1), abort);
-          const int s = idx % kSlots;
-          if (ok) ok = mbar_wait(full + 8 * s, (uint32_t)(idx / kSlots & 1), abort);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t v_at = sb + s * Sh::kSlot;
+        }
+        __syncwarp();
+        ++idx;
+        return true;
+      };
+      if (ok) ok = scores(step);
+      for (int c = walk.ca; ok && c < walk.cb; ++c, ++step) {
+        if (c + 1 < walk.cb) ok = scores(step + 1);
+        if (ok) ok = wait(sh.p_full, (uint32_t)(step & 1));
+        const int s = idx % kSlots;
+        if (ok) ok = wait(sh.full[s], (uint32_t)(idx / kSlots & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t v_at = desc_on(slots, s * Sh::kSlot);
+        if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < kTokens / 32; ++x)
-            mma_f8(o_tmem, rows_desc(v_at + x * 32 * D, D), rows_desc(sb + Sh::kOffP + x * 32, 128), kIdescO, c > walk.ca || x > 0);
+            mma_f8(o_tmem, desc_on(v_at, x * 32 * D), desc_on(p_desc, x * 32), kIdescO, c > walk.ca || x > 0);
           mma_commit(empty + 8 * s);
           mma_commit(smem_u32(&sh.o_done));
-          ++idx;
         }
+        __syncwarp();
+        ++idx;
       }
-      if (!ok) {
-        set_status(a.dev_status, DSPARK_ERR_DEVICE_TIMEOUT);
-        mma_commit(smem_u32(&sh.drain));
-        const long long begun = clock64();
-        while (!mbar_try(smem_u32(&sh.drain), 0) && clock64() - begun < kTimeoutCycles / 8) {
-        }
+    }
+    if (!ok && lane == 0) {
+      set_status(a.dev_status, DSPARK_ERR_DEVICE_TIMEOUT);
+      mma_commit(smem_u32(&sh.drain));
+      const long long begun = clock64();
+      while (!mbar_try(smem_u32(&sh.drain), 0) && clock64() - begun < kTimeoutCycles / 8) {
       }
     }
     __syncwarp();
   } else {
     // ---------------- scores to probabilities, sums to outputs ----------------
-    constexpr int NC = N / 2, kStep = NC < 16 ? 8 : 16;          // row-heads of a half, at once out of tensor memory
-    const int half = warp >> 2, col0 = half * NC, quad = warp & 3, t = tid & 127;
+    // Row-heads are dealt to the halves in groups of 8, so that those of a tile that is not full leave work to both.
+    constexpr int NG = N / 16, NC = 8 * NG;                      // groups and row-heads of a half
+    const int half = warp >> 2, quad = warp & 3, t = tid & 127;
+    auto col_of = [&](int g) { return 8 * (2 * g + half); };     // the first row-head of group g
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const int dim = D == 128 ? t : quad * 16 + lane;             // of O^T: with 64 dimensions 16 lanes of each warp
     const bool has_dim = D == 128 || lane < 16;
@@ -466,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
       fence_proxy_async_smem();
       sync_all();
       const bool some = walk.ca < walk.cb;
+      const int mine = (real + 7) / 8 > half ? ((real + 7) / 8 - half + 1) / 2 : 0;   // groups with row-heads
       if (some && lane == 0) mbar_arrive(smem_u32(&sh.q_ready));
       __syncwarp();
       float l[NC];
@@ -506,122 +505,149 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
         look_up();
         const int base = c * kTokens, tok = base + t;
         const bool edge = base < lo_max || base + kTokens > hi_min;
-        const bool mine_ok = mbar_wait(smem_u32(&sh.s_full[step & 1]), (uint32_t)(step >> 1 & 1), abort);
+        const bool mine_ok = mbar_try(smem_u32(&sh.s_full[step & 1]), (uint32_t)(step >> 1 & 1)) ||
+                             mbar_wait(smem_u32(&sh.s_full[step & 1]), (uint32_t)(step >> 1 & 1), abort);
         alive = __all_sync(0xffffffffu, mine_ok) && alive;
         tc_fence_after();
-        unsigned long long y[NC / 2];
-        {
-          const unsigned long long A2 = f2_pack(A, A);
-          uint32_t s[NC / kStep][kStep];
+        // `G` groups of row-heads (what P holds of others, past the last, reaches no output)
+        auto scores_to_terms = [&](auto groups) {
+          constexpr int G = decltype(groups)::value;
+          unsigned long long y[4 * G];
+          auto load_scores = [&]() {                             // the token's scores, scaled and masked
+            const unsigned long long A2 = f2_pack(A, A);
+            uint32_t s[G][8];
 #pragma unroll
-          for (int b = 0; b < NC / kStep; ++b) tmem_ld(tmem + lanes + (step & 1) * N + col0 + b * kStep, s[b]);
+            for (int g = 0; g < G; ++g) tmem_ld(tmem + lanes + (step & 1) * N + col_of(g), s[g]);
 #pragma unroll
-          for (int b = 0; b < NC / kStep; ++b) {
-            tmem_wait(s[b]);
+            for (int g = 0; g < G; ++g) {
+              tmem_wait(s[g]);
 #pragma unroll
-            for (int j = 0; j < kStep / 2; ++j)
-              y[b * kStep / 2 + j] = f2_mul(f2_pack(__uint_as_float(s[b][2 * j]), __uint_as_float(s[b][2 * j + 1])), A2);
-          }
-        }
-        if (edge) {
+              for (int j = 0; j < 4; ++j)
+                y[g * 4 + j] = f2_mul(f2_pack(__uint_as_float(s[g][2 * j]), __uint_as_float(s[g][2 * j + 1])), A2);
+            }
+            if (edge) {
 #pragma unroll
-          for (int j = 0; j < NC / 2; ++j) {
-            float y0, y1;
-            f2_unpack(y[j], y0, y1);
-            const int h0 = sh.hi[col0 + 2 * j], h1 = sh.hi[col0 + 2 * j + 1];
-            if (!(tok < h0 && (!a.window || tok >= h0 - a.window))) y0 = -INFINITY;
-            if (!(tok < h1 && (!a.window || tok >= h1 - a.window))) y1 = -INFINITY;
-            y[j] = f2_pack(y0, y1);
-          }
-        }
-        const ulonglong2 *Rs = reinterpret_cast<const ulonglong2 *>(sh.R + col0), *zs = reinterpret_cast<const ulonglong2 *>(sh.z + col0);
-        unsigned long long e[NC / 2];                            // exponents of the probabilities
-        auto exponents = [&]() {
-          float most = -INFINITY;
+              for (int j = 0; j < 4 * G; ++j) {
+                float y0, y1;
+                f2_unpack(y[j], y0, y1);
+                const int h0 = sh.hi[col_of(j / 4) + 2 * (j & 3)], h1 = sh.hi[col_of(j / 4) + 2 * (j & 3) + 1];
+                if (!(tok < h0 && (!a.window || tok >= h0 - a.window))) y0 = -INFINITY;
+                if (!(tok < h1 && (!a.window || tok >= h1 - a.window))) y1 = -INFINITY;
+                y[j] = f2_pack(y0, y1);
+              }
+              __syncwarp();
+            }
+          };
+          auto exponents = [&]() {                               // of their probabilities, in their place, and the largest
+            float most = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < NC / 4; ++j) {
-            const ulonglong2 r2 = Rs[j], z2 = zs[j];
-            float x0, x1, x2, x3;
-            e[2 * j] = f2_fma(y[2 * j], r2.x, z2.x);
-            e[2 * j + 1] = f2_fma(y[2 * j + 1], r2.y, z2.y);
-            f2_unpack(e[2 * j], x0, x1);
-            f2_unpack(e[2 * j + 1], x2, x3);
-            most = fmaxf(fmaxf(most, fmaxf(x0, x1)), fmaxf(x2, x3));
-          }
-          return most;
-        };
-        if (any_of_half(half, exponents() + lw > kBar)) {        // a reference moves
+            for (int j = 0; j < 2 * G; ++j) {
+              const int c2 = col_of(j / 2) + 4 * (j & 1);
+              const ulonglong2 r2 = *reinterpret_cast<const ulonglong2 *>(sh.R + c2), z2 = *reinterpret_cast<const ulonglong2 *>(sh.z + c2);
+              float x0, x1, x2, x3;
+              y[2 * j] = f2_fma(y[2 * j], r2.x, z2.x);
+              y[2 * j + 1] = f2_fma(y[2 * j + 1], r2.y, z2.y);
+              f2_unpack(y[2 * j], x0, x1);
+              f2_unpack(y[2 * j + 1], x2, x3);
+              most = fmaxf(fmaxf(most, fmaxf(x0, x1)), fmaxf(x2, x3));
+            }
+            return most;
+          };
+          // (one copy of the code whether a reference moves or not: what was loaded is loaded again then)
+          for (int round = 0;; ++round) {
+            load_scores();
+            if (round != 1) {
+              const float most = exponents();
+              if (round == 2 || !any_of_half(half, most + lw > kBar)) break;
+              continue;
+            }
+            // references move
 #pragma unroll
-          for (int j = 0; j < NC / 2; ++j) {
-            float y0, y1;
-            f2_unpack(y[j], y0, y1);
-            const int c2 = col0 + 2 * j;
-            float m2[2] = {fmaf(y0, sh.R[c2], lw), fmaf(y1, sh.R[c2 + 1], lw)};
+            for (int j = 0; j < 4 * G; ++j) {
+              const int c2 = col_of(j / 4) + 2 * (j & 3);
+              float y0, y1;
+              f2_unpack(y[j], y0, y1);
+              float m2[2] = {fmaf(y0, sh.R[c2], lw), fmaf(y1, sh.R[c2 + 1], lw)};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float x = m2[i] == m2[i] ? m2[i] : -INFINITY;
+              for (int i = 0; i < 2; ++i) {
+                float x = m2[i] == m2[i] ? m2[i] : -INFINITY;
 #pragma unroll
-              for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-              if (lane == 0) sh.most[quad][c2 + i] = x;
+                for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                if (lane == 0) sh.most[quad][c2 + i] = x;
+              }
+            }
+            sync_half(half);
+            if (t < 8 * G) {
+              const int c2 = col_of(t >> 3) + (t & 7);
+              const float was = sh.ref[c2];
+              const float up = fmaxf(fmaxf(fmaxf(sh.most[0][c2], sh.most[1][c2]), fmaxf(sh.most[2][c2], sh.most[3][c2])), was);
+              sh.factor[c2] = was == -INFINITY ? 0.0f : fast_ex2(was - up);
+              sh.ref[c2] = up;
+              if (up != -INFINITY && c2 < real) sh.z[c2] = kTop - up;
+            }
+            sync_half(half);
+#pragma unroll
+            for (int c = 0; c < 8 * G; ++c) l[c] *= sh.factor[col_of(c >> 3) + (c & 7)];
+            if (!at_first) {
+              const bool done = mbar_try(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1)) ||
+                              mbar_wait(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1), abort);
+              alive = __all_sync(0xffffffffu, done) && alive;
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < kTerms; ++i)
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                  const uint32_t o_at = o_tmem + lanes + i * N + col_of(g);
+                  uint32_t o[8];
+                  tmem_ld(o_at, o);
+                  tmem_wait(o);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.factor[col_of(g) + j]);
+                  tmem_st(o_at, o);
+                }
+              tmem_wait_st();
+              tc_fence_before();
             }
           }
-          sync_half(half);
-          if (t < NC) {
-            const int c2 = col0 + t;
-            const float was = sh.ref[c2];
-            const float up = fmaxf(fmaxf(fmaxf(sh.most[0][c2], sh.most[1][c2]), fmaxf(sh.most[2][c2], sh.most[3][c2])), was);
-            sh.factor[c2] = was == -INFINITY ? 0.0f : fast_ex2(was - up);
-            sh.ref[c2] = up;
-            if (up != -INFINITY && c2 < real) sh.z[c2] = kTop - up;
-          }
-          sync_half(half);
-#pragma unroll
-          for (int c2 = 0; c2 < NC; ++c2) l[c2] *= sh.factor[col0 + c2];
+          // probabilities in terms; the place of a byte in P: a row of 128, its 16-byte piece swizzled by the row
           if (!at_first) {
-            const bool done = mbar_wait(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1), abort);
+            const bool done = mbar_try(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1)) ||
+                              mbar_wait(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1), abort);
             alive = __all_sync(0xffffffffu, done) && alive;
-            tc_fence_after();
-#pragma unroll 1
-            for (int i = 0; i < kTerms; ++i)
-#pragma unroll
-              for (int b = 0; b < NC / kStep; ++b) {
-                const uint32_t o_at = o_tmem + lanes + i * N + col0 + b * kStep;
-                uint32_t o[kStep];
-                tmem_ld(o_at, o);
-                tmem_wait(o);
-#pragma unroll
-                for (int j = 0; j < kStep; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.factor[col0 + b * kStep + j]);
-                tmem_st(o_at, o);
-              }
-            tmem_wait_st();
-            tc_fence_before();
           }
-          exponents();
-        }
-        // probabilities in terms; the place of a byte in P: a row of 128, its 16-byte piece swizzled by the row
-        if (!at_first) {
-          const bool done = mbar_wait(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1), abort);
+          const unsigned long long w2 = f2_pack(w, w);
+          const uint32_t p_col = p_at + 8 * half * kTokens;
+#pragma unroll
+          for (int j = 0; j < 4 * G; ++j) {
+            constexpr int kGap = 16 * kTokens;
+            float x0, x1;
+            f2_unpack(y[j], x0, x1);
+            const float p0 = fast_ex2(x0), p1 = fast_ex2(x1);
+            l[2 * j] += p0;
+            l[2 * j + 1] += p1;
+            float v0, v1;
+            f2_unpack(f2_mul(f2_pack(p0, p1), w2), v0, v1);
+            uint32_t x[kTerms];
+            terms_of<kTerms, true>(pack_half2(v0, v1), x);
+            const uint32_t to0 = p_col + (t ^ ((2 * j & 7) << 4)) + j / 4 * kGap + 2 * (j & 3) * kTokens;
+            const uint32_t to1 = p_col + (t ^ (((2 * j + 1) & 7) << 4)) + j / 4 * kGap + (2 * (j & 3) + 1) * kTokens;
+#pragma unroll
+            for (int i = 0; i < kTerms; ++i) {
+              asm volatile("st.shared.u8 [%0], %1;" ::"r"(to0 + i * N * kTokens), "r"(x[i] >> 8) : "memory");
+              asm volatile("st.shared.u8 [%0], %1;" ::"r"(to1 + i * N * kTokens), "r"(x[i] >> 24) : "memory");
+            }
+          }
+        };
+        if (NG >= 4 && mine > 2)
+          scores_to_terms(std::integral_constant<int, NG>());
+        else if (NG >= 2 && mine > 1)
+          scores_to_terms(std::integral_constant<int, NG < 2 ? NG : 2>());
+        else if (mine > 0)
+          scores_to_terms(std::integral_constant<int, 1>());
+        else if (!at_first) {                                    // no row-head here: this half keeps pace
+          const bool done = mbar_try(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1)) ||
+                            mbar_wait(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1), abort);
           alive = __all_sync(0xffffffffu, done) && alive;
-        }
-        const unsigned long long w2 = f2_pack(w, w);
-        const uint32_t p_col = p_at + col0 * kTokens;
-#pragma unroll
-        for (int j = 0; j < NC / 2; ++j) {
-          float x0, x1;
-          f2_unpack(e[j], x0, x1);
-          const float p0 = fast_ex2(x0), p1 = fast_ex2(x1);
-          l[2 * j] += p0;
-          l[2 * j + 1] += p1;
-          float v0, v1;
-          f2_unpack(f2_mul(f2_pack(p0, p1), w2), v0, v1);
-          uint32_t x[kTerms];
-          terms_of<kTerms, true>(pack_half2(v0, v1), x);
-          const uint32_t to0 = p_col + (t ^ ((2 * j & 7) << 4)), to1 = p_col + (t ^ (((2 * j + 1) & 7) << 4));
-#pragma unroll
-          for (int i = 0; i < kTerms; ++i) {
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(to0 + (i * N + 2 * j) * kTokens), "r"(x[i] >> 8) : "memory");
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(to1 + (i * N + 2 * j + 1) * kTokens), "r"(x[i] >> 24) : "memory");
-          }
         }
         if (edge) {
           // A value of a token that no row of the tile sees is whatever the page held, one that some rows do not see
@@ -662,16 +688,18 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
 
       // ---------------- the piece's sums ----------------
       if (some) {
-        const bool done = mbar_wait(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1), abort);
+        const bool done = mbar_try(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1)) ||
+                            mbar_wait(smem_u32(&sh.o_done), (uint32_t)((step - 1) & 1), abort);
         alive = __all_sync(0xffffffffu, done) && alive;
         tc_fence_after();
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
+        if (col_of(c >> 3) >= real) break;
         float x = l[c];
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        if (lane == 0) sh.sum[quad][col0 + c] = x;
+        if (lane == 0) sh.sum[quad][col_of(c >> 3) + (c & 7)] = x;
       }
       sync_all();
       const bool whole = walk.begins && walk.ends, odd = *(volatile int *)&sh.odd != 0;
@@ -682,20 +710,20 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
       }
       __syncwarp();
 #pragma unroll 1
-      for (int b = 0; b < NC / kStep; ++b) {
-        const int c0 = col0 + b * kStep;
+      for (int g = 0; g < NG; ++g) {
+        const int c0 = col_of(g);
         if (c0 >= real) break;
-        float y[kStep];
+        float y[8];
 #pragma unroll
-        for (int j = 0; j < kStep; ++j) y[j] = 0.0f;
+        for (int j = 0; j < 8; ++j) y[j] = 0.0f;
         if (some) {
 #pragma unroll
           for (int i = 0; i < kTerms; ++i) {
-            uint32_t o[kStep];
+            uint32_t o[8];
             tmem_ld(o_tmem + lanes + i * N + c0, o);
             tmem_wait(o);
 #pragma unroll
-            for (int j = 0; j < kStep; ++j) y[j] += __uint_as_float(o[j]);
+            for (int j = 0; j < 8; ++j) y[j] += __uint_as_float(o[j]);
           }
         }
         if (odd && has_dim)
@@ -708,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
               const uint8_t held = a.data[((((int64_t)pg * a.Hkv + walk.h) * 2 + 1) * a.page_size + in) * D + piece * 16 + dim % 16];
               if ((held & 0x7f) != 0x7f) continue;
 #pragma unroll
-              for (int j = 0; j < kStep; ++j) {
+              for (int j = 0; j < 8; ++j) {
                 const int hi = sh.hi[c0 + j];
                 if (x < hi && (!a.window || x >= hi - a.window)) y[j] = __int_as_float(0x7fffffff);
               }
@@ -718,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DT, D, N>::kCtas)
         if (alive && has_dim) {
           int tok = (first + c0) / a.group, sub = first + c0 - tok * a.group;
 #pragma unroll
-          for (int j = 0; j < kStep; ++j) {
+          for (int j = 0; j < 8; ++j) {
             const int c = c0 + j;
             if (c >= real) break;
             if (whole) {
@@ -781,15 +809,24 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ ByteA
       f = l == 0.0f ? 0.0f : (m == -INFINITY || big == -INFINITY ? 1.0f : fast_ex2(m - big));
       sum = fmaf(l, f, sum);
     }
-    for (int p = 0; p < min(32, parts - p0); ++p) {
-      const float g = __shfl_sync(0xffffffffu, f, p);
-      if (g == 0.0f) continue;
-      const float2 *o = reinterpret_cast<const float2 *>(slot(p0 + p) + 2 * N + c * D + lane * kMine);
+    const int here = min(32, parts - p0);
+    for (int p1 = 0; p1 < here; p1 += 8) {                        // 8 pieces' rows under way
+      float2 u[8][kMine / 2];
 #pragma unroll
-      for (int i = 0; i < kMine; i += 2) {
-        const float2 u = o[i / 2];
-        y[i] = fmaf(u.x, g, y[i]);
-        y[i + 1] = fmaf(u.y, g, y[i + 1]);
+      for (int p = 0; p < 8; ++p)
+        if (p1 + p < here)
+#pragma unroll
+          for (int i = 0; i < kMine / 2; ++i)
+            u[p][i] = reinterpret_cast<const float2 *>(slot(p0 + p1 + p) + 2 * N + c * D + lane * kMine)[i];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const float g = __shfl_sync(0xffffffffu, f, (p1 + p) & 31);
+        if (p1 + p < here && g != 0.0f)
+#pragma unroll
+          for (int i = 0; i < kMine / 2; ++i) {
+            y[2 * i] = fmaf(u[p][i].x, g, y[2 * i]);
+            y[2 * i + 1] = fmaf(u[p][i].y, g, y[2 * i + 1]);
+          }
       }
     }
   }
