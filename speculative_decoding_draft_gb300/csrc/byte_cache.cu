@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   int64_t row = first, r = request_of_row(a.row_off, a.B, row, lane);
   const int64_t until = min(min(first + window, a.rows), all);
   const int half = a.rot / 2;
-  const bool turned = 8 * sub < a.rot;
+  const bool turned = 8 * sub < a.rot, all_turn = a.rot == D;
   const int other = !turned ? sub : (8 * sub < half ? sub + a.rot / 16 : sub - a.rot / 16);
   const float inv_d = 1.0f / (float)D;
   Eight<DT> w0 = {}, w1 = {};
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const Pair z = f2_fma(x[e], c[e], f2_mul(y[e], s[e]));
-        x[e] = turned ? z : x[e];
+        x[e] = all_turn || turned ? z : x[e];
       }
     }
   };
@@ -251,13 +251,14 @@ __global__ void __launch_bounds__(kThreads, 3)
 
     // queries: a row's head takes LANES lanes, four steps under way
     const int units = len * nq;
+    const uint32_t inv_nq = nq > 1 ? 0xffffffffu / nq + 1 : 0;   // u / nq = high word of the product, u nq being below 2^32
     for (int u0 = warp * 4 * kBeside; u0 < units; u0 += kWarps * 4 * kBeside) {
       Eight<DT> in[4];
       int j[4], h[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int u = min(u0 + k * kBeside + beside, units - 1);
-        j[k] = u / nq;
+        j[k] = nq > 1 ? (int)__umulhi((uint32_t)u, inv_nq) : u;
         h[k] = q0 + u - j[k] * nq;
         in[k] = load8_once<DT>(reinterpret_cast<const T *>(a.q) + (row + j[k]) * a.q_row + h[k] * a.q_head + 8 * sub);
       }
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(128) read_kernel(const __grid_constant__ ByteR
 template <int DT, int D>
 cudaError_t append(const ByteHeadsArgs &a, cudaStream_t s, int sms) {
   // windows of rows until two waves of CTAs are full, then heads shared out where rows are few
-  const int64_t enough = 6 * (int64_t)sms;
+  const int64_t enough = 6 * (int64_t)sms;          // (12, 24 and 48: 9216 rows 149, 155 and 168 us, 8190 rows 31, 37 and 48 against 29)
   int window = 16, parts = 1;
   while (window > 1 && (a.rows + window - 1) / window < enough) window /= 2;
   const int64_t windows = (a.rows + window - 1) / window;

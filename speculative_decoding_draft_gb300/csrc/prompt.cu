@@ -431,23 +431,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = warp >> 2, t = threadIdx.x & 127, q4 = warp & 3;
     const Tile tile = i ? tile_b : tile_a;
     if (i < tiles) {
-      // queries: 16 bytes at a time, neighbouring threads along a row, 8 loads under way
+      // queries: 16 bytes at a time, neighbouring threads along a row, all of a thread's loads under way
       const T *q = reinterpret_cast<const T *>(a.q) + (int64_t)h * a.group * a.q_head;
       constexpr int kPieces = D / 8;
-#pragma unroll 1
-      for (int p0 = t; p0 < kTileRows * kPieces; p0 += 8 * kTileRows) {
-        uint4 x[8];
+      {
+        uint4 x[kPieces];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int p = p0 + u * kTileRows, rho = first + i * kTileRows + p / kPieces, tok = rho / a.group;
+        for (int u = 0; u < kPieces; ++u) {
+          const int p = t + u * kTileRows, rho = first + i * kTileRows + p / kPieces, tok = rho / a.group;
           x[u] = make_uint4(0, 0, 0, 0);
           if (rho < total)
             x[u] = __ldg(reinterpret_cast<const uint4 *>(q + (row0 + tok) * a.q_row + (int64_t)(rho - tok * a.group) * a.q_head +
                                                          p % kPieces * 8));
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int p = p0 + u * kTileRows, row = p / kPieces, c = p % kPieces;
+        for (int u = 0; u < kPieces; ++u) {
+          const int p = t + u * kTileRows, row = p / kPieces, c = p % kPieces;
           *reinterpret_cast<uint4 *>(gb + i * Sh::kQ + c / 8 * (kTileRows * 128) + row * 128 + ((c % 8) ^ (row & 7)) * 16) = x[u];
         }
       }
