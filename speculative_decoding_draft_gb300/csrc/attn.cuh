@@ -123,6 +123,7 @@ struct PromptArgs {
   int64_t B, rows, kv_rows, units;
   int Hq, Hkv, D, group, causal, window, dtype, parts;
   int k_x, k_z, v_x, v_z;             // a head's place in the tensor copies' coordinates
+  uint32_t group_inv;                 // ceil(2^32 / group), 0 for 1
   float scale_log2;
   float *partial;                     // workspace of the split form
   int32_t *dev_status;

@@ -35,6 +35,7 @@ constexpr int kTileRows = 128;
 constexpr int kUnitRows = 2 * kTileRows;
 constexpr int kThreads = 12 * 32;
 constexpr float kLazy = 8.0f;              // how far (log2) a score may pass the running maximum
+constexpr float kNear = 4.0f;              // how far a first maximum may lie below 0 and 0 be taken for it
 
 template <int D>
 struct Shape {
@@ -102,6 +103,11 @@ __device__ __forceinline__ int end_of(const PromptArgs &a, int ctx, int kv, int 
   return a.causal ? ctx + rho / a.group + 1 : kv;
 }
 __device__ __forceinline__ int start_of(const PromptArgs &a, int end) { return a.window ? max(end, a.window) - a.window : 0; }
+
+// The token of a row-head among the first few (a CTA's): `on` / group, by a product, exact while on group is below 2^32.
+__device__ __forceinline__ int token_of(const PromptArgs &a, int on) {
+  return a.group > 1 ? (int)__umulhi((uint32_t)on, a.group_inv) : on;
+}
 
 // What a tile's row-heads see: from lo_max at the latest up to [hi_min, hi_max], in steps [t0, t1).
 struct Tile {
@@ -215,22 +221,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       sh.request = r;
       sh.tile = unit - ((int64_t)a.row_off[r] * a.group / kUnitRows + r);
+    }
+  } else if (warp == 1) {                                        // beside the search
+    if (lane < kSlots) {
+      mbar_init(smem_u32(&sh.full[lane]), 1);
+      mbar_init(smem_u32(&sh.empty[lane]), 3);                   // the products and both looking warps
+      mbar_init(smem_u32(&sh.v_fine[lane]), 2);
+    }
+    if (lane < 2) {
+      mbar_init(smem_u32(&sh.q_full[lane]), kTileRows);
+      mbar_init(smem_u32(&sh.s_full[lane]), 1);
+      mbar_init(smem_u32(&sh.p_full[lane]), 4);
+      mbar_init(smem_u32(&sh.o_full[lane]), 1);
+    }
+    if (lane == 0) {
+      mbar_init(smem_u32(&sh.drain), 1);
       sh.abort = sh.odd = 0;
       sh.skip = read_status(a.dev_status);
-      for (int i = 0; i < kSlots; ++i) {
-        mbar_init(smem_u32(&sh.full[i]), 1);
-        mbar_init(smem_u32(&sh.empty[i]), 3);                  // the products and both looking warps
-        mbar_init(smem_u32(&sh.v_fine[i]), 2);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(smem_u32(&sh.q_full[i]), kTileRows);
-        mbar_init(smem_u32(&sh.s_full[i]), 1);
-        mbar_init(smem_u32(&sh.p_full[i]), 4);
-        mbar_init(smem_u32(&sh.o_full[i]), 1);
-      }
-      mbar_init(smem_u32(&sh.drain), 1);
-      fence_barrier_init();
     }
+    __syncwarp();
+    fence_barrier_init();
   }
   __syncthreads();
   if (sh.skip) return;
@@ -434,14 +444,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // queries: 16 bytes at a time, neighbouring threads along a row, all of a thread's loads under way
       const T *q = reinterpret_cast<const T *>(a.q) + (int64_t)h * a.group * a.q_head;
       constexpr int kPieces = D / 8;
+      const int skipped = first / a.group * a.group;             // row-heads of tokens before the CTA's first
+      const int64_t q_row0 = row0 + first / a.group;
       {
         uint4 x[kPieces];
 #pragma unroll
         for (int u = 0; u < kPieces; ++u) {
-          const int p = t + u * kTileRows, rho = first + i * kTileRows + p / kPieces, tok = rho / a.group;
+          const int p = t + u * kTileRows, rho = first + i * kTileRows + p / kPieces;
+          const int on = rho - skipped, tok = token_of(a, on);
           x[u] = make_uint4(0, 0, 0, 0);
           if (rho < total)
-            x[u] = __ldg(reinterpret_cast<const uint4 *>(q + (row0 + tok) * a.q_row + (int64_t)(rho - tok * a.group) * a.q_head +
+            x[u] = __ldg(reinterpret_cast<const uint4 *>(q + (q_row0 + tok) * a.q_row + (int64_t)(on - tok * a.group) * a.q_head +
                                                          p % kPieces * 8));
         }
 #pragma unroll
@@ -459,8 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
       const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * 128;
       const float R = a.scale_log2;
-      // probabilities are 2^(s R + z), z = kLift - the running maximum; no maximum yet: z = 0
-      float top = -INFINITY, z = 0.0f, l = 0.0f;
+      // probabilities are 2^(s R + z), z = kLift - the running maximum; none yet: -inf and z = 0.  The first step is taken
+      // against 0, which serves as well where a row's largest score (log2) lies near it.
+      float top = 0.0f, z = kLift, l = 0.0f;
       uint32_t turn = 0;
       bool ok = true;
       for (int c = tile.t0; c < tile.t1; ++c) {
@@ -471,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const bool at_edge = tile.edge(c);
         const int cols = tile.columns(c), lo = start - c * kTokens, hi = end - c * kTokens;
-        bool measure = c == tile.t0;                             // the maximum first
+        bool measure = false;
         uint32_t P[64];
         float more;
         for (;;) {
@@ -522,7 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             take_step<DT, false>(s_at, kTokens, 0, 0, R, z, P, most, more);
           // (a first maximum of -inf leaves the next step to measure; an infinite score measured leaves it at that)
-          if (measure || !__any_sync(0xffffffffu, most > kLift + kLazy || (top == -INFINITY && most > -INFINITY))) break;
+          const bool far = c == tile.t0 ? real && !(most >= kLift - kNear && most <= kLift + kLazy)
+                                        : most > kLift + kLazy || (top == -INFINITY && most > -INFINITY);
+          if (measure || !__any_sync(0xffffffffu, far)) break;
+          if (c == tile.t0) top = -INFINITY, z = 0.0f;
           measure = true;
         }
         l += more;
@@ -584,13 +601,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (split) {
 #pragma unroll
               for (int k = 0; k < 32; k += 2) *reinterpret_cast<float2 *>(partial + 2 + b * 32 + k) = make_float2(y[k], y[k + 1]);
-            } else {
-              uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(a.out) + to * D + b * 32);
+            } else {                                             // into the place of the tile's queries, swizzled by the row
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                dst[k] = make_uint4(pack_pair<DT>(y[8 * k], y[8 * k + 1]), pack_pair<DT>(y[8 * k + 2], y[8 * k + 3]),
-                                    pack_pair<DT>(y[8 * k + 4], y[8 * k + 5]), pack_pair<DT>(y[8 * k + 6], y[8 * k + 7]));
+                *reinterpret_cast<uint4 *>(gb + i * Sh::kQ + t * (2 * D) + ((b * 4 + k) ^ (t & 7)) * 16) =
+                    make_uint4(pack_pair<DT>(y[8 * k], y[8 * k + 1]), pack_pair<DT>(y[8 * k + 2], y[8 * k + 3]),
+                               pack_pair<DT>(y[8 * k + 4], y[8 * k + 5]), pack_pair<DT>(y[8 * k + 6], y[8 * k + 7]));
             }
+          }
+        }
+        __syncwarp();
+        if (!split) {                                            // whole rows at a time: the warp's 32
+          constexpr int kLanes = D / 8;
+          const int skipped = first / a.group * a.group;
+          T *out = reinterpret_cast<T *>(a.out) + ((row0 + first / a.group) * a.Hq + h * a.group) * D;
+#pragma unroll
+          for (int x = lane; x < 32 * kLanes; x += 32) {
+            const int row = q4 * 32 + x / kLanes, piece = x % kLanes, rho2 = first + i * kTileRows + row;
+            const int on = rho2 - skipped, tok2 = token_of(a, on);
+            if (rho2 < total)
+              *reinterpret_cast<uint4 *>(out + ((int64_t)tok2 * a.Hq + on - tok2 * a.group) * D + piece * 8) =
+                  *reinterpret_cast<const uint4 *>(gb + i * Sh::kQ + row * (2 * D) + (piece ^ (row & 7)) * 16);
           }
         }
         if (real) {
@@ -717,6 +748,7 @@ cudaError_t launch_prompt(const PromptArgs &args, cudaStream_t s, int sms) {
   PromptArgs a = args;
   a.units = units_of(a.rows, a.B, a.group);
   a.parts = parts_of(a.units * a.Hkv, a.kv_rows, a.B, sms);
+  a.group_inv = a.group > 1 ? 0xffffffffu / (unsigned)a.group + 1 : 0;
   CUtensorMap k = {}, v = {};
   if (a.kv_rows > 0 && (!encode(&k, a.k, a, a.k_row, a.k_head, &a.k_x, &a.k_z) ||
                         !encode(&v, a.v, a, a.v_row, a.v_head, &a.v_x, &a.v_z)))
