@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (;;) {
           if (measure) {
             float most = -INFINITY;
-#pragma unroll
+#pragma unroll 1
             for (int b = 0; b < 4; ++b) {
               if (b * 32 >= cols) break;
               uint32_t s[32];
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool risen = up > top;
             if (c > tile.t0 && __any_sync(0xffffffffu, risen)) {
               // O of the steps before is complete: S of this one came after it
-#pragma unroll
+#pragma unroll 1
               for (int b = 0; b < D / 32; ++b) {
                 uint32_t o[32];
                 tmem_ld32(o_at + b * 32, o);
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool odd = *(volatile int *)&sh.odd != 0, split = a.parts > 1;
         const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
         float *partial = split ? a.partial + ((int64_t)part * a.rows * a.Hq + to) * (D + 2) : nullptr;
-#pragma unroll
+#pragma unroll 1                                                 // (unrolled, the code comes into the cache late)
         for (int b = 0; b < D / 32; ++b) {
           __syncwarp();                                          // (the load takes the warp together)
           uint32_t o[32];
