@@ -1,9 +1,9 @@
 """Speculative decoding of a small random target model, with every operator of the verification step.
 
-    python examples/verification_step.py [--steps 8] [--temperature 0.0]
+    python examples/verification_step.py [--steps 8] [--temperature 0.0] [--bits 4]
 
 Each step drafts up to K tokens a request, schedules how many of them to verify, runs the target model over
-the ragged rows (per layer: project, norm, rotate and append in one call, attend over the 4-bit cache),
+the ragged rows (per layer: project, norm, rotate and append in one call, attend over the cache, of 4 or 8 bits),
 penalises and masks the rows' logits, and accepts or rejects.  Rejected tokens need no clean-up: the next
 step's rows take their places in the cache.
 """
@@ -22,7 +22,7 @@ import speculative_decoding_draft_gb300 as ds  # noqa: E402
 class Target:
     """A decoder of random weights: attention layers with normed, rotated heads and a gated residual."""
 
-    def __init__(self, B, V=512, layers=2, hq=4, hkv=2, d=64, page=16, most=512, seed=0):
+    def __init__(self, B, V=512, layers=2, hq=4, hkv=2, d=64, page=16, most=512, seed=0, bits=4):
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
         w = hq * d
@@ -37,7 +37,8 @@ class Target:
                             qn=(1 + normal(d, std=0.1)), kn=(1 + normal(d, std=0.1))) for _ in range(layers)]
         per = -(-most // page)
         self.table = torch.randperm(B * per, generator=g, device="cuda").to(torch.int32).view(B, per)
-        self.caches = [ds.PagedCache.empty(B * per, hkv, d, page, k_scale=0.25, v_scale=0.25) for _ in range(layers)]
+        self.caches = [ds.PagedCache8.empty(B * per, hkv, d, page) if bits == 8 else
+                       ds.PagedCache.empty(B * per, hkv, d, page, k_scale=0.25, v_scale=0.25) for _ in range(layers)]
         self.rope = ds.Rope(d, base=1e4, scaling="yarn", factor=4.0, original_len=128)
         self.status = ds.new_status("cuda")
 
@@ -143,9 +144,10 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=8)
     ap.add_argument("--temperature", type=float, default=0.0)
+    ap.add_argument("--bits", type=int, default=4, choices=(4, 8))
     a = ap.parse_args()
     B, K = 6, 4
-    t = Target(B)
+    t = Target(B, bits=a.bits)
     dec = Decoder(t, [[7 + r, 11, 3 * r] + list(range(r)) for r in range(B)])
     for i in range(a.steps):
         n, ell = dec.step(draft_model(B, K, t.V, seed=5 + i), K, a.temperature)

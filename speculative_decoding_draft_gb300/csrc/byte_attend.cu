@@ -25,6 +25,12 @@
 // CTAs fit on the GPU: lengths need not be alike for all to end together, and one long request fills the GPU by
 // itself.  A unit that is cut leaves its pieces' sums in a workspace, where join_kernel adds them in order.
 //
+// Measured (one GB300): one request of 131071 tokens with 8 rows, 32 query and 8 key/value heads of 128 dimensions, 85 us
+// (40 us of reading at the memory's rate); 64 requests of 512 to 4096 tokens with 1 to 8 rows 141 us (46); 256 requests
+// of up to 16384 tokens, heads of 64 dimensions, 672 us (359).  Bound by a step's chain (scores out of tensor memory,
+// exponents, terms, stores, products) with two CTAs an SM, and by what a piece costs before and after its steps.  One
+// group of four warps on all row-heads took 112, 198 and 822 us.
+//
 // Warps 0-3 and 4-7: half of the row-heads each; a thread has a token of S^T (scales, mask, exponentials, terms of P),
 // then a dimension of O^T.  Warp 8 brings keys and values by bulk copies into a ring, looking up pages a step ahead.
 // Warp 9 issues the products: S of the next step before P V of this one.

@@ -13,6 +13,10 @@
 // known only when all of them are (held in registers between the two, 16 rows took 128 registers a thread, and
 // half the warps on an SM); queries go row by row.  A lane holds 8 neighbouring dimensions.
 //
+// Measured (one GB300): 9216 rows of 2048 requests with 32 query and 8 key/value heads of 128 dimensions 111 us (30 us at
+// the memory's rate), bound by issue slots (52 % busy) and by a run's steps that follow one another (look-up, angles, two
+// sweeps, queries); their read-back with the rest of the touched blocks 35 us (22), bound by the look-up's latency.
+//
 // All arithmetic is in fp32; queries are rounded once to their type, keys and values once to 8 bits, and once more
 // where a block's scale rises behind them.
 #include "heads.cuh"

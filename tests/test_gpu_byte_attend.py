@@ -250,3 +250,21 @@ def test_a_prompt_in_pieces_then_decoding(dtype):
         bound = bound + (half(dt) + 2.0 ** -10) * 4 * math.sqrt(d) * 2.0 ** -3
         assert ((got.double() - out).abs() <= bound).all()
         done = kv
+
+
+def test_the_example_decodes_over_8_bits():
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    try:
+        import verification_step as example
+    finally:
+        sys.path.pop(0)
+    B, K = 5, 3
+    dec = example.Decoder(example.Target(B, bits=8), [[7 + r, 11, 3 * r] + list(range(r)) for r in range(B)])
+    for i in range(6):
+        dec.step(example.draft_model(B, K, dec.t.V, seed=9 + i), K, 0.0)
+    assert ds.check(dec.t.status) == "DSPARK_OK"
+    for r in range(B):                                           # the grammar holds along every emitted token
+        out = dec.text[r, int(dec.prompt[r]) - 1: int(dec.length[r])]
+        assert len(out) > 6 and ((out[1:] + out[:-1]) % 2 == 1).all()
