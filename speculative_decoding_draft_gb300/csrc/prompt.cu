@@ -19,8 +19,8 @@
 // The running maximum moves only when a score passes it by 2^8, so that probabilities are computed against the
 // maximum as it stands while they are checked; a warp with a row that passes takes its 32 rows again.
 //
-// Measured (one GB300): 16384 tokens, 32 query and 8 key/value heads of 128 dimensions, causal, 1679 us, 1310 TFLOP/s
-// (1145 us at the rate of a large plain product); 16 prompts of 127 to 1021 tokens 127 us.  Bound by the chain of a tile
+// Measured (one GB300): 16384 tokens, 32 query and 8 key/value heads of 128 dimensions, causal, 1682 us, 1308 TFLOP/s
+// (1145 us at the rate of a large plain product); 16 prompts of 127 to 1021 tokens 140 us.  Bound by the chain of a tile
 // (scores 512 cycles, softmax 1250, products 512, and the waits between them) of which two run beside each other, and
 // for short prompts by what a CTA does before its first product (9000 cycles) and after its last (5000).  Two tiles
 // that share loaded keys and values rather than one: each 32 KB that arrives serves 256 row-heads, and 512 columns of
