@@ -577,7 +577,8 @@ dspark_status dspark_attn_paged_byte(const dspark_heads *q, int32_t q_heads, int
  * head i / (q_heads / kv_heads): row j of n_r sees tokens t < hi, hi = m_r (causal: m_r - n_r + j + 1), and with
  * window > 0 only t >= hi - window.  A row that sees nothing gets 0 and lse -inf.  What masked tokens hold,
  * infinities and NaN included, changes nothing.  lse [rows, q_heads] float, optional: log sum exp(scale q.k).
- * row_off, kv_off [B+1] int32, not falling; rows of out at and past row_off[B] are left alone.  D 64 or 128; rows *
+ * row_off, kv_off [B+1] int32, not falling; rows of out at and past row_off[B] are left alone; out may be q's memory
+ * where that is contiguous.  D 64 or 128; rows *
  * q_heads / kv_heads < 2^31 - 256.  k and v have their heads inside the rows (all of a row's heads before the next
  * row), or their rows inside the heads with the head's stride a multiple of the row's; no stride is 0 (broadcast).
  * BF16, F16.

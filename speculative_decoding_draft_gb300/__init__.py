@@ -25,8 +25,8 @@ __all__ = [
     "verify_ragged", "check", "status_string", "draft_workspace_bytes", "schedule_workspace_bytes",
     "verify_workspace_bytes", "F32", "BF16", "FLAG_FORCE_SIMT", "FLAG_W_PACKED", "FLAG_SPARE_SM", "STATUS_NAMES", "Dims",
     "PackedProjection", "pack_projection", "packed_projection_bytes", "verify_markov",
-    "verify_markov_workspace_bytes", "Rope", "PagedCache", "norm_rope", "cache_append", "cache_read", "attend_paged",
-    "penalize_logits", "F16",
+    "verify_markov_workspace_bytes", "Rope", "PagedCache", "PagedCache8", "norm_rope", "cache_append", "cache_read", "attend_paged",
+    "attend_prompt", "penalize_logits", "F16",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

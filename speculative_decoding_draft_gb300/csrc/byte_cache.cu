@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int part = (int)(blockIdx.x % (unsigned)parts);
   const int q0 = a.Hq * part / parts, nq = a.Hq * (part + 1) / parts - q0;
   const int h0 = a.Hkv * part / parts, nkv = a.Hkv * (part + 1) / parts - h0;
-  if (status_on_entry(a.dev_status)) return;
+  // (the word may change while the CTA's threads read it: they leave together or not at all)
+  if (__syncthreads_or(status_on_entry(a.dev_status))) return;
 
   // Runs begin where a request does and at every block's first token.
   const int64_t all = a.row_off[a.B];

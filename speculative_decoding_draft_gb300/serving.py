@@ -350,8 +350,8 @@ def attend_prompt(q, k, v, row_off, *, kv_off=None, scale: Optional[float] = Non
     the last where there are more (a later piece of a prompt over its earlier ones).  scale: 1/sqrt(D) unless given.
     Row j of n sees its request's m tokens up to m - n + j (causal) or all, and with window > 0 only the last
     ``window`` of them; a row that sees nothing gets 0 and lse -inf, and what masked tokens hold (infinities, NaN)
-    changes nothing.  Returns out [rows, Hq, D] and, with want_lse, lse [rows, Hq] float32.  Rows at and past row_off[B]
-    are left alone.
+    changes nothing.  Returns out [rows, Hq, D] (``out`` may name q itself where that is contiguous) and, with want_lse, lse [rows, Hq] float32.  Rows
+    at and past row_off[B] are left alone.
     """
     return _done(_native().prompt(q, k, v, row_off, kv_off, scale, causal, window, want_lse, out, workspace, status,
                                   _raw(stream)), "dspark_attn_prompt")

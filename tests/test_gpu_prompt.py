@@ -274,3 +274,28 @@ def test_another_stream_and_a_graph():
     q.copy_(randn(g, 330, 4, 128))
     graph.replay()
     assert torch.equal(held["out"], ds.attend_prompt(q, k, v, off)["out"])
+
+
+def test_infinities_where_the_tokens_are_shared_out():
+    # few rows over many tokens: a value that only the last row sees, in the last part
+    g, m = gen(11), 9000
+    q = randn(g, 3, 4, 128).bfloat16()
+    k, v = randn(g, m, 1, 128).bfloat16(), randn(g, m, 1, 128).bfloat16()
+    clean = ds.attend_prompt(q, k, v, offsets([3]), kv_off=offsets([m]))
+    assert clean["workspace"] is not None
+    v[m - 1, 0, 7], v[m - 2, 0, 9] = math.inf, math.nan
+    got = ds.attend_prompt(q, k, v, offsets([3]), kv_off=offsets([m]))
+    ok(got["status"])
+    same = torch.ones_like(q, dtype=torch.bool)
+    same[2, :, 7] = same[1:, :, 9] = False
+    assert torch.equal(got["out"][same], clean["out"][same])
+    assert (got["out"][2, :, 7] == math.inf).all() and torch.isnan(got["out"][1:, :, 9]).all()
+
+
+def test_the_output_may_be_the_queries():
+    g, n = gen(12), [300, 20]
+    q, k, v = randn(g, 320, 4, 64).half(), randn(g, 320, 2, 64).half(), randn(g, 320, 2, 64).half()
+    want = ds.attend_prompt(q, k, v, offsets(n))["out"]
+    got = ds.attend_prompt(q, k, v, offsets(n), out=dict(out=q))
+    ok(got["status"])
+    assert got["out"].data_ptr() == q.data_ptr() and torch.equal(q, want)
